@@ -23,12 +23,23 @@ FA_ERR_CUDA = 4
 FA_ERR_DEVICE_TIMEOUT = 5
 FA_ERR_WORKSPACE_LIMIT = 6
 FA_ERR_SCHED_BUSY = 7
+FA_ERR_BAD_PAGE = 8
 FA_STATIC_WORKSPACE_BYTES = 64 * 1024 * 1024   # include/fa.h
 FA_O_F32 = 0
 FA_O_BF16 = 1
 FA_IN_BF16 = 0
 FA_IN_E4M3 = 1
 FA_FLAG_EAGER_RESCALE = 1
+FA_T_BF16 = 0
+FA_T_F32 = 1
+FA_ROTARY_HALF = 0
+FA_ROTARY_INTERLEAVED = 1
+FA_ROTARY_NONE = 0
+FA_ROTARY_LINEAR = 1
+FA_ROTARY_BASE = 2
+FA_ROTARY_PARTS = 3
+FA_ROTARY_MAX_DIM = 256
+FA_ROPE_MAX_D = 1024
 
 _lock = threading.Lock()
 _lib = None
@@ -68,6 +79,75 @@ class FaBwdParams(ctypes.Structure):
         ("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int), ("d", ctypes.c_int),
         ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("o_dtype", ctypes.c_int),
         ("timeout_ms", ctypes.c_uint32), ("H_kv", ctypes.c_int), ("N_k", ctypes.c_int),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class FaRotarySpec(ctypes.Structure):
+    """Mirror of fa_rotary_spec."""
+    _fields_ = [
+        ("dim", ctypes.c_int), ("layout", ctypes.c_int), ("base", ctypes.c_double), ("scaling", ctypes.c_int),
+        ("factor", ctypes.c_double), ("original_length", ctypes.c_double), ("low_turns", ctypes.c_double),
+        ("high_turns", ctypes.c_double), ("amplitude", ctypes.c_double),
+        ("angles", ctypes.POINTER(ctypes.c_double)),
+    ]
+
+
+class FaRotary(ctypes.Structure):
+    """Mirror of fa_rotary."""
+    _fields_ = [
+        ("dim", ctypes.c_int), ("layout", ctypes.c_int), ("amplitude", ctypes.c_float), ("ready", ctypes.c_int),
+        ("step", ctypes.c_uint64 * (FA_ROTARY_MAX_DIM // 2)),
+    ]
+
+
+class FaRopeTensor(ctypes.Structure):
+    """Mirror of fa_rope_tensor."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
+
+
+class FaRopeParams(ctypes.Structure):
+    """Mirror of fa_rope_params."""
+    _fields_ = [
+        ("t", FaRopeTensor * 2), ("B", ctypes.c_int), ("N", ctypes.c_int), ("d", ctypes.c_int),
+        ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int), ("pos", ctypes.c_void_p),
+        ("pos_stride", ctypes.c_int64), ("pos0", ctypes.c_int32), ("inverse", ctypes.c_int),
+        ("rotary", ctypes.POINTER(FaRotary)),
+    ]
+
+
+class FaCache(ctypes.Structure):
+    """Mirror of fa_cache."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("n_pages", ctypes.c_int),
+        ("max_pages", ctypes.c_int), ("B", ctypes.c_int), ("H_kv", ctypes.c_int), ("page", ctypes.c_int),
+        ("d", ctypes.c_int),
+    ]
+
+
+class FaCacheAppendParams(ctypes.Structure):
+    """Mirror of fa_cache_append_params."""
+    _fields_ = [
+        ("cache", FaCache), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
+        ("v_stride", ctypes.c_int64 * 3), ("N", ctypes.c_int), ("start", ctypes.c_void_p),
+        ("n_new", ctypes.c_void_p), ("rotary", ctypes.POINTER(FaRotary)), ("dev_status", ctypes.c_void_p),
+    ]
+
+
+class FaCacheGatherParams(ctypes.Structure):
+    """Mirror of fa_cache_gather_params."""
+    _fields_ = [("cache", FaCache), ("k_len", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("N_k", ctypes.c_int), ("dev_status", ctypes.c_void_p)]
+
+
+class FaCacheAttnParams(ctypes.Structure):
+    """Mirror of fa_cache_attn_params."""
+    _fields_ = [
+        ("cache", FaCache), ("q", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("k_len", ctypes.c_void_p), ("dev_status", ctypes.c_void_p), ("H", ctypes.c_int), ("N", ctypes.c_int),
+        ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("o_dtype", ctypes.c_int),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
@@ -114,6 +194,18 @@ def load():
             lib.fa_testhook_sched_next_slot.argtypes = []
             lib.fa_testhook_sched_slot.restype = i
             lib.fa_testhook_sched_slot.argtypes = [i, vp, vp]
+            lib.fa_rotary_init.restype = i
+            lib.fa_rotary_init.argtypes = [ctypes.POINTER(FaRotary), ctypes.POINTER(FaRotarySpec)]
+            lib.fa_rope.restype = i
+            lib.fa_rope.argtypes = [ctypes.POINTER(FaRopeParams), vp]
+            lib.fa_cache_append.restype = i
+            lib.fa_cache_append.argtypes = [ctypes.POINTER(FaCacheAppendParams), vp]
+            lib.fa_cache_gather.restype = i
+            lib.fa_cache_gather.argtypes = [ctypes.POINTER(FaCacheGatherParams), vp]
+            lib.fa_cache_attn.restype = i
+            lib.fa_cache_attn.argtypes = [ctypes.POINTER(FaCacheAttnParams), vp]
+            lib.fa_cache_attn_workspace_bytes.restype = ctypes.c_size_t
+            lib.fa_cache_attn_workspace_bytes.argtypes = [ctypes.POINTER(FaCacheAttnParams)]
             _lib = lib
     return _lib
 

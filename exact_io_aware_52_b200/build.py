@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libfa_sm100.so")
 SELFTEST_LIB = os.path.join(HERE, "libfa_selftest.so")
 # library -> its translation units
 TARGETS = {
-    LIB: [os.path.join(CSRC, "fa_api.cu"), os.path.join(CSRC, "fa_static_workspace.cu")],
+    LIB: [os.path.join(CSRC, "fa_api.cu"), os.path.join(CSRC, "fa_static_workspace.cu"),
+          os.path.join(CSRC, "fa_rope.cu"), os.path.join(CSRC, "fa_cache.cu")],
     SELFTEST_LIB: [os.path.join(CSRC, "selftest.cu")],
 }
 HEADERS = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + \

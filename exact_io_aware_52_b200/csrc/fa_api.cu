@@ -21,7 +21,7 @@
 namespace {
 
 constexpr int kVersion = 300;  // 0.3.0
-constexpr int kMaxDevices = 64;
+using fa_detail::kMaxDevices;
 constexpr int kMaxSplits = 1024;
 
 // Scheduler slots of the dynamic work distribution (causal forward, backward):
@@ -318,6 +318,14 @@ fa_status probe_current_device() {
     DeviceInfo *di = nullptr;
     std::lock_guard<std::mutex> lk(g_mu);
     return probe_device(&dev, &di);
+}
+
+fa_status current_device(int *dev, int *num_sms) {
+    DeviceInfo *di = nullptr;
+    std::lock_guard<std::mutex> lk(g_mu);
+    const fa_status st = probe_device(dev, &di);
+    if (st == FA_OK) *num_sms = di->num_sms;
+    return st;
 }
 
 }  // namespace fa_detail
@@ -739,7 +747,7 @@ fa_status fa_read_device_status(const int32_t *dev_status, void *stream) {
     int32_t h = 0;
     if (cudaMemcpyAsync(&h, dev_status, sizeof h, cudaMemcpyDeviceToHost, s) != cudaSuccess) return FA_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return FA_ERR_CUDA;
-    if (h != FA_OK && h != FA_ERR_DEVICE_TIMEOUT && h != FA_ERR_SCHED_BUSY) return FA_ERR_CUDA;
+    if (h != FA_OK && h != FA_ERR_DEVICE_TIMEOUT && h != FA_ERR_SCHED_BUSY && h != FA_ERR_BAD_PAGE) return FA_ERR_CUDA;
     return (fa_status)h;
 }
 
@@ -753,6 +761,7 @@ const char *fa_status_string(fa_status s) {
         case FA_ERR_DEVICE_TIMEOUT: return "FA_ERR_DEVICE_TIMEOUT";
         case FA_ERR_WORKSPACE_LIMIT: return "FA_ERR_WORKSPACE_LIMIT";
         case FA_ERR_SCHED_BUSY: return "FA_ERR_SCHED_BUSY";
+        case FA_ERR_BAD_PAGE: return "FA_ERR_BAD_PAGE";
     }
     return "FA_ERR_UNKNOWN";
 }

@@ -1,0 +1,275 @@
+// fa_cache.cu -- the paged 8-bit key/value cache: argument checks and launches
+// of fa_cache_append, fa_cache_gather and fa_cache_attn.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "fa.h"
+#include "fa_cache_attn_kernel.cuh"
+#include "fa_cache_kernels.cuh"
+#include "fa_internal.h"
+
+namespace {
+
+using fa_detail::aligned;
+using fa_detail::kMaxDevices;
+
+constexpr long long kMaxInt = 0x7fffffffLL;
+
+int log2_of(int x) {
+    int r = 0;
+    while ((1 << r) < x) ++r;
+    return r;
+}
+
+fa_status validate_cache(const fa_cache *c) {
+    if (c->B < 0 || c->H_kv < 0 || c->n_pages < 0 || c->max_pages < 0 || c->table_stride < 0)
+        return FA_ERR_INVALID_ARGUMENT;
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return FA_ERR_UNSUPPORTED;
+    if (c->d != 64 && c->d != 128 && c->d != 256) return FA_ERR_UNSUPPORTED;
+    if ((long long)c->max_pages * c->page > kMaxInt || (long long)c->B * c->H_kv > kMaxInt)
+        return FA_ERR_INVALID_ARGUMENT;
+    if (c->B == 0 || c->H_kv == 0) return FA_OK;
+    if (c->n_pages > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)) return FA_ERR_INVALID_ARGUMENT;
+    if (c->max_pages > 0 && !c->table) return FA_ERR_INVALID_ARGUMENT;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_MISALIGNED;
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !aligned(c->table, 4)) return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+
+fa::CacheView view_of(const fa_cache &c) {
+    fa::CacheView v;
+    v.k = static_cast<uint8_t *>(c.k);
+    v.v = static_cast<uint8_t *>(c.v);
+    v.k_scale = c.k_scale;
+    v.v_scale = c.v_scale;
+    v.table = c.table;
+    v.table_stride = c.table_stride;
+    v.n_pages = c.n_pages;
+    v.max_pages = c.max_pages;
+    v.B = c.B;
+    v.H_kv = c.H_kv;
+    v.page = c.page;
+    v.d = c.d;
+    v.page_log2 = log2_of(c.page);
+    return v;
+}
+
+// 16-byte aligned base and strides of whole 16 bytes, where there is more than one entry.
+bool vectors(const void *base, const int64_t *stride, int B, int H, int N) {
+    const int n[3] = {B, H, N};
+    if (!aligned(base, 16)) return false;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && stride[i] % 8 != 0) return false;
+    return true;
+}
+
+template <int SPT>
+void launch_append(const fa::AppendParams &kp, bool vec, unsigned grid, int threads, cudaStream_t s) {
+    if (vec)
+        fa::fa_cache_append_kernel<SPT, true><<<grid, threads, 0, s>>>(kp);
+    else
+        fa::fa_cache_append_kernel<SPT, false><<<grid, threads, 0, s>>>(kp);
+}
+
+// ---------------------------------------------------------------- attention
+struct AttnPlan {
+    int nt, rows, chunks, workers;
+    size_t o_bytes, ml_bytes;
+};
+
+// CTAs that one SM holds (the kernel's launch bounds).
+int attn_occupancy(int d, int nt) { return d == 256 ? 2 : (nt == 2 ? 3 : 4); }
+
+AttnPlan plan_attn(const fa_cache_attn_params *p, int resident) {
+    namespace ca = fa::cattn;
+    AttnPlan a;
+    const fa_cache &c = p->cache;
+    a.rows = p->H / c.H_kv * p->N;
+    a.nt = (a.rows <= 8 || c.d == 256) ? 1 : 2;
+    a.chunks = (a.rows + 8 * a.nt - 1) / (8 * a.nt);
+    long long w = resident / a.chunks;
+    const long long tiles = (long long)c.B * c.H_kv * (((long long)c.max_pages * c.page) / ca::kTile);
+    const long long most = (tiles + ca::kWarps - 1) / ca::kWarps;  // a worker takes a tile for each warp at least
+    if (w > most) w = most;
+    a.workers = w < 1 ? 1 : (int)w;
+    const size_t slots = (size_t)a.chunks * a.workers * 2 * 8 * a.nt;
+    a.o_bytes = slots * c.d * sizeof(float);
+    a.ml_bytes = slots * 2 * sizeof(float);
+    return a;
+}
+
+bool attn_empty(const fa_cache_attn_params *p) {
+    return p->cache.B == 0 || p->cache.H_kv == 0 || p->H == 0 || p->N == 0;
+}
+
+template <int D, int NT>
+fa_status launch_attn(const fa::cattn::Params &kp, int dev, cudaStream_t s) {
+    namespace ca = fa::cattn;
+    static std::atomic<bool> ready[kMaxDevices];
+    auto kern = ca::fa_cache_attn_kernel<D, NT>;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ca::kSmemBytes<D>) != cudaSuccess)
+            return FA_ERR_CUDA;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    kern<<<kp.chunks * kp.workers, ca::kThreads, ca::kSmemBytes<D>, s>>>(kp);
+    if (cudaPeekAtLastError() != cudaSuccess) return FA_ERR_CUDA;
+
+    // The merge is launched while the first kernel runs and waits in it for its results.
+    // One warp for a row, or eight where few (sequence, head) pairs mean many parts each.
+    const long long rows = (long long)kp.c.B * kp.c.H_kv * kp.rows;
+    const bool wide = kp.workers > 8LL * kp.c.B * kp.c.H_kv;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + ca::kMergeWarps - 1) / ca::kMergeWarps));
+    cfg.blockDim = dim3(32 * ca::kMergeWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, ca::fa_cache_merge_kernel<D, ca::kMergeWarps>, kp, 8 * NT)
+                               : cudaLaunchKernelEx(&cfg, ca::fa_cache_merge_kernel<D, 1>, kp, 8 * NT);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_cache_append(const fa_cache_append_params *p, void *stream) {
+    if (!p || p->N < 0) return FA_ERR_INVALID_ARGUMENT;
+    fa_status st = validate_cache(&p->cache);
+    if (st != FA_OK) return st;
+    const fa_cache &c = p->cache;
+    if (p->rotary && (st = fa_detail::validate_rotary(p->rotary, c.d)) != FA_OK) return st;
+    if (c.B == 0 || c.H_kv == 0 || p->N == 0) return FA_OK;
+    if (!p->k || !p->v || !p->start) return FA_ERR_INVALID_ARGUMENT;
+    if (!aligned(p->k, 2) || !aligned(p->v, 2) || !aligned(p->start, 4) || !aligned(p->n_new, 4) ||
+        !aligned(p->dev_status, 4))
+        return FA_ERR_MISALIGNED;
+    int dev = 0, sms = 0;
+    if ((st = fa_detail::current_device(&dev, &sms)) != FA_OK) return st;
+
+    fa::AppendParams kp;
+    std::memset(&kp, 0, sizeof kp);
+    kp.c = view_of(c);
+    kp.x[0] = static_cast<const uint16_t *>(p->k);
+    kp.x[1] = static_cast<const uint16_t *>(p->v);
+    for (int i = 0; i < 3; ++i) {
+        kp.xs[0][i] = p->k_stride[i];
+        kp.xs[1][i] = p->v_stride[i];
+    }
+    kp.N = p->N;
+    // N tokens that begin in the last slot of a page
+    kp.pages = (int)(((long long)p->N - 1 + c.page - 1) / c.page) + 1;
+    kp.start = p->start;
+    kp.n_new = p->n_new;
+    kp.status = p->dev_status;
+    bool vec = vectors(p->k, p->k_stride, c.B, c.H_kv, p->N) && vectors(p->v, p->v_stride, c.B, c.H_kv, p->N);
+    if (p->rotary) {
+        kp.dim = p->rotary->dim;
+        kp.interleaved = p->rotary->layout == FA_ROTARY_INTERLEAVED;
+        kp.amplitude = p->rotary->amplitude;
+        std::memcpy(kp.step, p->rotary->step, sizeof(uint64_t) * (kp.dim / 2));
+        vec = vec && kp.dim % 16 == 0;
+    }
+    const long long blocks = 2LL * c.B * c.H_kv * kp.pages;
+    if (blocks > kMaxInt) return FA_ERR_INVALID_ARGUMENT;
+    const int slots = c.page * (c.d / 16);  // 64 .. 2048 of 16 components
+    const int threads = slots < 512 ? slots : 512;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    switch (slots / threads) {
+        case 1: launch_append<1>(kp, vec, (unsigned)blocks, threads, s); break;
+        case 2: launch_append<2>(kp, vec, (unsigned)blocks, threads, s); break;
+        default: launch_append<4>(kp, vec, (unsigned)blocks, threads, s); break;
+    }
+    return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_cache_gather(const fa_cache_gather_params *p, void *stream) {
+    if (!p || p->N_k < 0) return FA_ERR_INVALID_ARGUMENT;
+    fa_status st = validate_cache(&p->cache);
+    if (st != FA_OK) return st;
+    const fa_cache &c = p->cache;
+    if (c.B == 0 || c.H_kv == 0 || p->N_k == 0) return FA_OK;
+    if (!p->k || !p->v || !p->k_len) return FA_ERR_INVALID_ARGUMENT;
+    if (!aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->k_len, 4) || !aligned(p->dev_status, 4))
+        return FA_ERR_MISALIGNED;
+    int dev = 0, sms = 0;
+    if ((st = fa_detail::current_device(&dev, &sms)) != FA_OK) return st;
+    fa::GatherParams kp;
+    std::memset(&kp, 0, sizeof kp);
+    kp.c = view_of(c);
+    kp.k_len = p->k_len;
+    kp.k = static_cast<uint16_t *>(p->k);
+    kp.v = static_cast<uint16_t *>(p->v);
+    kp.N_k = p->N_k;
+    kp.status = p->dev_status;
+    const int per_block = fa::kGatherThreads * fa::kGatherItems / (c.d / 16);
+    kp.row_blocks = (int)(((long long)p->N_k + per_block - 1) / per_block);
+    const long long blocks = (long long)c.B * c.H_kv * kp.row_blocks;
+    if (blocks > kMaxInt) return FA_ERR_INVALID_ARGUMENT;
+    fa::fa_cache_gather_kernel<<<(unsigned)blocks, fa::kGatherThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(kp);
+    return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_cache_attn_workspace_bytes(const fa_cache_attn_params *p) {
+    if (!p || validate_cache(&p->cache) != FA_OK || p->H <= 0 || p->N <= 0 || p->cache.B == 0 || p->cache.H_kv == 0 ||
+        p->H % p->cache.H_kv != 0 || (long long)p->H / p->cache.H_kv * p->N > kMaxInt)
+        return 0;
+    const AttnPlan a = plan_attn(p, fa::cattn::kMaxWorkers);
+    return a.o_bytes + a.ml_bytes;
+}
+
+fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream) {
+    if (!p || p->H < 0 || p->N < 0) return FA_ERR_INVALID_ARGUMENT;
+    fa_status st = validate_cache(&p->cache);
+    if (st != FA_OK) return st;
+    const fa_cache &c = p->cache;
+    if ((p->causal != 0 && p->causal != 1) || !std::isfinite(p->scale) || p->scale <= 0.f)
+        return FA_ERR_INVALID_ARGUMENT;
+    if (p->o_dtype != FA_O_F32 && p->o_dtype != FA_O_BF16) return FA_ERR_INVALID_ARGUMENT;
+    if (attn_empty(p)) return FA_OK;
+    if (p->H % c.H_kv != 0 || (long long)c.B * p->H > kMaxInt / p->N) return FA_ERR_INVALID_ARGUMENT;
+    if (!p->q || !p->o || !p->lse || !p->k_len || !p->workspace) return FA_ERR_INVALID_ARGUMENT;
+    if (!aligned(p->q, 16) || !aligned(p->o, 16) || !aligned(p->workspace, 16) || !aligned(p->lse, 4) ||
+        !aligned(p->k_len, 4) || !aligned(p->dev_status, 4))
+        return FA_ERR_MISALIGNED;
+    if (p->workspace_bytes < fa_cache_attn_workspace_bytes(p)) return FA_ERR_INVALID_ARGUMENT;
+    int dev = 0, sms = 0;
+    if ((st = fa_detail::current_device(&dev, &sms)) != FA_OK) return st;
+
+    AttnPlan a = plan_attn(p, fa::cattn::kMaxWorkers);
+    const int resident = attn_occupancy(c.d, a.nt) * sms;
+    if (resident < fa::cattn::kMaxWorkers) a = plan_attn(p, resident);
+    fa::cattn::Params kp;
+    std::memset(&kp, 0, sizeof kp);
+    kp.c = view_of(c);
+    kp.q = static_cast<const uint16_t *>(p->q);
+    kp.o = p->o;
+    kp.lse = p->lse;
+    kp.k_len = p->k_len;
+    kp.status = p->dev_status;
+    kp.o_part = static_cast<float *>(p->workspace);
+    kp.ml_part = reinterpret_cast<float2 *>(static_cast<char *>(p->workspace) + a.o_bytes);
+    kp.N = p->N;
+    kp.rows = a.rows;
+    kp.chunks = a.chunks;
+    kp.workers = a.workers;
+    kp.causal = p->causal;
+    kp.o_bf16 = p->o_dtype == FA_O_BF16;
+    kp.scale_log2 = (float)((double)p->scale * 1.4426950408889634074);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    switch (c.d) {
+        case 64: return a.nt == 1 ? launch_attn<64, 1>(kp, dev, s) : launch_attn<64, 2>(kp, dev, s);
+        case 128: return a.nt == 1 ? launch_attn<128, 1>(kp, dev, s) : launch_attn<128, 2>(kp, dev, s);
+        default: return launch_attn<256, 1>(kp, dev, s);
+    }
+}
+
+}  // extern "C"

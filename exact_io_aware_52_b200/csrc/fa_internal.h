@@ -14,4 +14,15 @@ fa_status validate_args(const fa_fwd_params *p);
 // (cached per device ordinal); FA_ERR_UNSUPPORTED or FA_ERR_CUDA otherwise.
 fa_status probe_current_device();
 
+// The same, with the device's ordinal and its number of SMs.
+fa_status current_device(int *dev, int *num_sms);
+
+// Device ordinals are below this (current_device refuses others).
+constexpr int kMaxDevices = 64;
+
+inline bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// The rule of fa_rotary_init's result (rotary->ready and its dim within d).
+fa_status validate_rotary(const fa_rotary *r, int d);
+
 }  // namespace fa_detail

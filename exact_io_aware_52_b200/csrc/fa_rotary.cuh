@@ -1,0 +1,86 @@
+// fa_rotary.cuh -- the rotation of rotary positions, shared by fa_rope and
+// fa_cache_append.
+//
+// The angle of pair i at position p is p * w_i.  A float (or a double, for a
+// far position and fast pairs) would lose its fraction of a turn, so the
+// table holds w_i as a 64-bit fraction of a turn and the product p * step is
+// taken modulo 2^64: the wrap-around drops the whole turns exactly, and the
+// error left is |p| * 2^-65 turns (2^-34 at p = 2^31).  The product's high
+// word is the angle in [-1/2, 1/2) turns, and sincospi takes it in half turns.
+#pragma once
+
+#include <cstdint>
+
+#include "sm100_ptx.cuh"
+
+namespace fa {
+
+// cos and sin of position * step, times the amplitude.
+__device__ __forceinline__ void rotary_cs(uint64_t step, int pos, float amplitude, float sign, float &c, float &s) {
+    const uint64_t turns = step * (uint64_t)(int64_t)pos;
+    sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f /* 2^-31 */, &s, &c);
+    c *= amplitude;
+    s *= amplitude * sign;
+}
+
+// (a, b) -> (a c - b s, b c + a s), the products in fp32.
+__device__ __forceinline__ void rotary_turn(float &a, float &b, float c, float s) {
+    const float x = a, y = b;
+    a = fmaf(x, c, -(y * s));
+    b = fmaf(y, c, x * s);
+}
+
+// A head's components are handled in slots of 16: two runs of 8 components
+// that hold whole pairs, so that one thread reads, turns and writes a slot by
+// itself.  Needs d and dim to be multiples of 16.  A rotated slot s < dim / 16
+// holds the 8 pairs from 8 s: with the half layout components [8 s, 8 s + 8)
+// and the same dim / 2 further on, else [16 s, 16 s + 16).  The others pass.
+struct RotarySlot {
+    int a, b;      // first component of each run
+    bool rotated;
+};
+__device__ __forceinline__ RotarySlot rotary_slot(int s, int dim, bool interleaved) {
+    RotarySlot r;
+    r.rotated = s < (dim >> 4);
+    const bool split = r.rotated && !interleaved;
+    r.a = split ? 8 * s : 16 * s;
+    r.b = split ? 8 * s + (dim >> 1) : 16 * s + 8;
+    return r;
+}
+
+// Turns a slot's 16 components in place: pair j is (v[j], v[8 + j]) or (v[2 j], v[2 j + 1]).
+__device__ __forceinline__ void rotary_turn_slot(float (&v)[16], const float (&c)[8], const float (&s)[8],
+                                                 bool interleaved) {
+    if (interleaved) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rotary_turn(v[2 * j], v[2 * j + 1], c[j], s[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rotary_turn(v[j], v[8 + j], c[j], s[j]);
+    }
+}
+
+// 8 components at p (16-byte aligned for bf16, 32 bytes read for fp32).
+__device__ __forceinline__ void load8(const uint16_t *p, float *v) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    v[0] = bf16x2_lo(u.x), v[1] = bf16x2_hi(u.x), v[2] = bf16x2_lo(u.y), v[3] = bf16x2_hi(u.y);
+    v[4] = bf16x2_lo(u.z), v[5] = bf16x2_hi(u.z), v[6] = bf16x2_lo(u.w), v[7] = bf16x2_hi(u.w);
+}
+__device__ __forceinline__ void load8(const float *p, float *v) {
+    const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+}
+__device__ __forceinline__ void store8(uint16_t *p, const float *v) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float *p, const float *v) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.f); }
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+
+}  // namespace fa

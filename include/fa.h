@@ -65,9 +65,11 @@ typedef enum {
     FA_ERR_DEVICE_TIMEOUT = 5,   /* (device status word) a pipeline wait timed out     */
     FA_ERR_WORKSPACE_LIMIT = 6,  /* fa_fwd_static_workspace: the splits need more than
                                     FA_STATIC_WORKSPACE_BYTES of scratch                */
-    FA_ERR_SCHED_BUSY = 7        /* (device status word) the launch's scheduler slot stayed
+    FA_ERR_SCHED_BUSY = 7,       /* (device status word) the launch's scheduler slot stayed
                                     in use by another in-flight launch for longer than the
                                     wait limit; the launch did no work                  */
+    FA_ERR_BAD_PAGE = 8          /* (device status word) a page-table entry outside
+                                    [0, n_pages), or a position outside the table       */
 } fa_status;
 
 typedef enum { FA_O_F32 = 0, FA_O_BF16 = 1 } fa_o_dtype;
@@ -305,6 +307,202 @@ FA_EXPORT fa_status fa_bwd(const fa_bwd_params *p, void *stream);
  * FA_ERR_WORKSPACE_LIMIT, and FA_ERR_CUDA if the lookup fails.
  */
 FA_EXPORT fa_status fa_fwd_static_workspace(const fa_fwd_params *p, void *stream);
+
+/*
+ * Rotary positions.  Component pair i of a head's first `dim` components is
+ * turned by the angle position * w_i:
+ *     (a, b) -> m * (a cos - b sin, b cos + a sin)
+ * (m the amplitude), which makes q . k of two turned heads a function of the
+ * distance of their positions.  The components from `dim` on pass unchanged.
+ */
+typedef enum {
+    FA_ROTARY_HALF = 0,       /* pair i is (x[i], x[i + dim / 2])  */
+    FA_ROTARY_INTERLEAVED = 1 /* pair i is (x[2 i], x[2 i + 1])    */
+} fa_rotary_layout;
+
+/* How w_i = base^(-2 i / dim) is changed for contexts longer than the original length. */
+typedef enum {
+    FA_ROTARY_NONE = 0,   /* w_i                                                        */
+    FA_ROTARY_LINEAR = 1, /* w_i / factor (positions interpolated)                      */
+    FA_ROTARY_BASE = 2,   /* base * factor^(dim / (dim - 2)) in place of base: the
+                             slowest pair is divided by factor, the fastest kept        */
+    FA_ROTARY_PARTS = 3   /* by turns_i = original_length * w_i / 2 pi: w_i / factor up
+                             to low_turns, w_i from high_turns on, and linear in turns_i
+                             between the two                                            */
+} fa_rotary_scaling;
+
+typedef struct {
+    int dim;                 /* rotated leading components: even, 2 .. FA_ROTARY_MAX_DIM */
+    int layout;              /* fa_rotary_layout                                        */
+    double base;             /* > 0, finite (10000 is common)                           */
+    int scaling;             /* fa_rotary_scaling                                       */
+    double factor;           /* > 0, finite; unused by FA_ROTARY_NONE                   */
+    double original_length;  /* FA_ROTARY_PARTS: > 0                                    */
+    double low_turns, high_turns; /* FA_ROTARY_PARTS: 0 <= low < high                   */
+    double amplitude;        /* m above; 0 means 1; finite, >= 0                        */
+    const double *angles;    /* host, w_i in radians for each of the dim / 2 pairs, or
+                                NULL.  If given, base and scaling are not used; finite,
+                                |w_i| <= 2^20                                           */
+} fa_rotary_spec;
+
+#define FA_ROTARY_MAX_DIM 256
+
+/* A rotation ready for use: a plain value that the caller keeps and may copy. */
+typedef struct {
+    int dim, layout;
+    float amplitude;
+    int ready;                              /* set by fa_rotary_init                    */
+    uint64_t step[FA_ROTARY_MAX_DIM / 2];   /* w_i in units of 2^-64 turn: position * step
+                                               modulo 2^64 is the angle without the whole
+                                               turns, exact however far the position    */
+} fa_rotary;
+
+/* fa_rotary_init -- fills *r from *spec.  Host arithmetic only. */
+FA_EXPORT fa_status fa_rotary_init(fa_rotary *r, const fa_rotary_spec *spec);
+
+/* Element type of a plain tensor. */
+typedef enum { FA_T_BF16 = 0, FA_T_F32 = 1 } fa_dtype;
+
+typedef struct {
+    const void *x;           /* device [B, heads, N, d] by strides, x_dtype             */
+    void *y;                 /* device [B, heads, N, d] by strides, y_dtype; may be x
+                                itself (same type and strides), else no overlap         */
+    int heads;               /* >= 0; 0: the tensor is absent                           */
+    int64_t x_stride[3];     /* elements from one batch element, head, token to the next
+                                (components are contiguous); any order of dimensions    */
+    int64_t y_stride[3];
+} fa_rope_tensor;
+
+typedef struct {
+    fa_rope_tensor t[2];     /* queries and keys, say; one launch turns both            */
+    int B, N, d;             /* d: rotary dim .. FA_ROPE_MAX_D                          */
+    int x_dtype, y_dtype;    /* fa_dtype                                                */
+    const int32_t *pos;      /* device int32 positions, pos[b * pos_stride + n], or NULL:
+                                the position of token n is pos0 + n                     */
+    int64_t pos_stride;      /* 0: one row of positions for the whole batch             */
+    int32_t pos0;
+    int inverse;             /* 1: turn by the negative angles (with the amplitude, the
+                                transpose: what the gradient of the turned tensor needs)*/
+    const fa_rotary *rotary; /* host                                                    */
+} fa_rope_params;
+
+#define FA_ROPE_MAX_D 1024
+
+/*
+ * fa_rope -- one launch.  The products are formed in fp32 from the inputs and
+ * rounded once to y_dtype.  No alignment beyond the element type is needed;
+ * 16-byte aligned tensors with strides of whole 16 bytes, and d and dim that
+ * are multiples of 16, are read and written 16 bytes at a time.
+ */
+FA_EXPORT fa_status fa_rope(const fa_rope_params *p, void *stream);
+
+/*
+ * A paged key/value cache in 8 bits.  Token t of sequence b lies in slot
+ * t % page of page table[b * table_stride + t / page]; a page has, for every
+ * key/value head, `page` slots of d E4M3 codes, and one scale: the value is
+ * code * scale.  The caller owns all of it and says which pages a sequence
+ * has; several sequences may share pages that are only read.
+ */
+typedef struct {
+    void *k, *v;               /* device E4M3 [n_pages, H_kv, page, d], 16-byte aligned  */
+    float *k_scale, *v_scale;  /* device fp32 [n_pages, H_kv]                            */
+    const int32_t *table;      /* device int32 [B, max_pages]; entries past a sequence's
+                                  last page are not read                                 */
+    int64_t table_stride;      /* elements from one row of the table to the next         */
+    int n_pages, max_pages;
+    int B, H_kv, page, d;      /* page in {16, 32, 64, 128}, d in {64, 128, 256}         */
+} fa_cache;
+
+typedef struct {
+    fa_cache cache;
+    const void *k, *v;         /* device bf16 [B, H_kv, N, d] by strides                 */
+    int64_t k_stride[3], v_stride[3]; /* elements from one batch element, head, token to
+                                  the next (components are contiguous)                   */
+    int N;                     /* tokens given for each sequence                         */
+    const int32_t *start;      /* device int32 [B]: position of the first new token, that
+                                  is the tokens that the sequence holds already          */
+    const int32_t *n_new;      /* device int32 [B] or NULL (N): of each sequence's N
+                                  tokens the first n_new[b] are written (clamped to
+                                  [0, N]), the others are not read                       */
+    const fa_rotary *rotary;   /* host, or NULL; turns each key by its position on the way
+                                  (dim <= d)                                             */
+    int32_t *dev_status;       /* device status word or NULL, as in fa_fwd_params        */
+} fa_cache_append_params;
+
+/*
+ * fa_cache_append -- writes new tokens into the cache; one launch.
+ *
+ * The scale of a page and head is a power of two, 2^e with the least
+ * e >= -100 for which the largest finite magnitude of its values is at most
+ * 448 * 2^e (E4M3's largest code).  A page that holds tokens from before
+ * keeps the larger of its scale and that; if it grows, the codes of those
+ * tokens (slots below the first new one) are rescaled, which for
+ * power-of-two scales is exact but for codes that become subnormal.  A page
+ * whose slot 0 is written has no scale from before.  Infinities and NaN
+ * become the code NaN.  Slots behind the last new token are left as they are.
+ *
+ * A token whose position is negative or past the table, or whose page is
+ * outside [0, n_pages), is not written and FA_ERR_BAD_PAGE is stored in
+ * *dev_status.  Two sequences must not append to the same page in one call.
+ */
+FA_EXPORT fa_status fa_cache_append(const fa_cache_append_params *p, void *stream);
+
+typedef struct {
+    fa_cache cache;
+    const int32_t *k_len;      /* device int32 [B]: tokens that each sequence holds,
+                                  clamped to [0, max_pages * page]                       */
+    void *k, *v;               /* device bf16 [B, H_kv, N_k, d], contiguous, 16-byte
+                                  aligned                                                */
+    int N_k;
+    int32_t *dev_status;
+} fa_cache_gather_params;
+
+/*
+ * fa_cache_gather -- the cache's first N_k tokens of every sequence as
+ * contiguous keys and values, the form that fa_fwd_ex reads (with k_len);
+ * zero behind a sequence's end.  Exact for the scales that fa_cache_append
+ * writes; code * scale rounded once for any others.  The tokens of a page
+ * outside [0, n_pages) read as zero and store FA_ERR_BAD_PAGE.
+ */
+FA_EXPORT fa_status fa_cache_gather(const fa_cache_gather_params *p, void *stream);
+
+typedef struct {
+    fa_cache cache;            /* scales: finite, >= 0                                   */
+    const void *q;             /* device bf16 [B, H, N, d], contiguous, 16-byte aligned  */
+    void *o;                   /* device [B, H, N, d], fp32 or bf16 per o_dtype          */
+    float *lse;                /* device fp32 [B, H, N]                                  */
+    const int32_t *k_len;      /* device int32 [B]: tokens that each sequence holds, the
+                                  N queries' own included; clamped to
+                                  [0, max_pages * page]                                  */
+    int32_t *dev_status;
+    int H, N;                  /* query heads (a multiple of H_kv) and query tokens      */
+    int causal;                /* 1: query i of sequence b sits at position
+                                  k_len[b] - N + i and sees the keys up to itself        */
+    float scale;               /* finite, > 0                                            */
+    int o_dtype;               /* fa_o_dtype                                             */
+    void *workspace;           /* device scratch, 16-byte aligned, at least
+                                  fa_cache_attn_workspace_bytes(p) bytes; owned by the
+                                  caller, nothing in it has to be set, and not shared by
+                                  calls whose executions overlap                         */
+    size_t workspace_bytes;
+} fa_cache_attn_params;
+
+/* Scratch bytes fa_cache_attn needs for *p; host arithmetic only; 0 for a NULL p. */
+FA_EXPORT size_t fa_cache_attn_workspace_bytes(const fa_cache_attn_params *p);
+
+/*
+ * fa_cache_attn -- attention of a few query tokens for each sequence over the
+ * cache, O and lse as in fa_fwd.  Made for decoding: the keys are split
+ * evenly over the whole GPU whatever the sequences' lengths, each key and
+ * value is read once for all the query heads that share it, and the parts are
+ * merged by a second launch.  For the many tokens of a prompt, fa_fwd_ex on
+ * the contiguous keys (fa_cache_gather) is the faster call.  Sums, softmax
+ * statistics and products accumulate in fp32; the weights are rounded to
+ * fp16 before the product with the values.  A row with no allowed key gets
+ * O = 0, lse = -inf.  The keys of a page outside [0, n_pages) are left out
+ * and FA_ERR_BAD_PAGE is stored.  Results do not depend on timing.
+ */
+FA_EXPORT fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream);
 
 /*
  * Test hooks (not for production use): the scheduler slot the next causal
