@@ -148,7 +148,8 @@ class FaCacheAttnParams(ctypes.Structure):
         ("cache", FaCache), ("q", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p),
         ("k_len", ctypes.c_void_p), ("dev_status", ctypes.c_void_p), ("H", ctypes.c_int), ("N", ctypes.c_int),
         ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("o_dtype", ctypes.c_int),
-        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("timeout_ms", ctypes.c_uint32),
+        ("test_drop_load", ctypes.c_int),
     ]
 
 

@@ -261,7 +261,7 @@ def cache_attention_workspace_bytes(cache, H, N):
 
 
 def cache_attention(cache, q, k_len, causal, scale, *, out_dtype=None, out=None, workspace=None, dev_status=None,
-                    stream=None):
+                    timeout_ms=0, stream=None, test_drop_load=0):
     """fa_cache_attn: attention of N query tokens for each sequence over the cache.
 
     q: bf16 [B, H, N, d], contiguous, H a multiple of the cache's heads.  k_len:
@@ -269,7 +269,8 @@ def cache_attention(cache, q, k_len, causal, scale, *, out_dtype=None, out=None,
     query i of sequence b sits at position k_len[b] - N + i.  Returns O in
     out_dtype (fp32 default) and lse (fp32 [B, H, N]), or writes the pair `out`.  workspace: a
     tensor of cache_attention_workspace_bytes bytes, not shared by calls that overlap
-    (two captured graphs, say); allocated for the call by default.
+    (two captured graphs, say); allocated for the call by default.  dev_status: int32 status
+    word for FA_ERR_BAD_PAGE and FA_ERR_DEVICE_TIMEOUT (a wait longer than timeout_ms, 0 = 2000).
     """
     dev = cache.device_index
     _need(q.dim() == 4 and q.dtype == torch.bfloat16 and q.is_contiguous() and q.get_device() == dev,
@@ -290,10 +291,10 @@ def cache_attention(cache, q, k_len, causal, scale, *, out_dtype=None, out=None,
         _need(workspace.is_contiguous() and workspace.get_device() == dev,
               "workspace must be contiguous and on the same device")
     return _run(dev, stream, _attention, cache, q, _ints(k_len, "k_len", (B,), dev), int(bool(causal)), float(scale),
-                out, o_type, workspace, _ints(dev_status, "dev_status", (1,), dev), dev)
+                out, o_type, workspace, _ints(dev_status, "dev_status", (1,), dev), timeout_ms, test_drop_load, dev)
 
 
-def _attention(cache, q, k_len, causal, scale, out, o_type, workspace, dev_status, dev):
+def _attention(cache, q, k_len, causal, scale, out, o_type, workspace, dev_status, timeout_ms, test_drop_load, dev):
     B, H, N, d = q.shape
     if out is None:
         out = (torch.empty((B, H, N, d), dtype=o_type, device=q.device),
@@ -303,6 +304,6 @@ def _attention(cache, q, k_len, causal, scale, out, o_type, workspace, dev_statu
     p = fb.FaCacheAttnParams(cache.struct, q.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), k_len, dev_status, H, N,
                              causal, scale, fb.FA_O_BF16 if o_type == torch.bfloat16 else fb.FA_O_F32,
                              workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size())
+                             workspace.numel() * workspace.element_size(), timeout_ms, test_drop_load)
     fb._check(fb.load().fa_cache_attn(p, _raw_stream(dev)), "fa_cache_attn")
     return tuple(out)

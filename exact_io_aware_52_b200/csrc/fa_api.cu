@@ -328,6 +328,22 @@ fa_status current_device(int *dev, int *num_sms) {
     return st;
 }
 
+fa_status encode_cache_map(CUtensorMap *map, const void *codes, long long tiles, int lines, int line_bytes) {
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        const fa_status st = load_encoder();
+        if (st != FA_OK) return st;
+    }
+    cuuint64_t dims[3] = {(cuuint64_t)line_bytes, (cuuint64_t)lines, (cuuint64_t)tiles};
+    cuuint64_t strides[2] = {(cuuint64_t)line_bytes, (cuuint64_t)line_bytes * lines};
+    cuuint32_t box[3] = {128, (cuuint32_t)lines, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(codes), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 }  // namespace fa_detail
 
 extern "C" {

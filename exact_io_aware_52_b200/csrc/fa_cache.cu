@@ -32,6 +32,8 @@ fa_status validate_cache(const fa_cache *c) {
     if (c->d != 64 && c->d != 128 && c->d != 256) return FA_ERR_UNSUPPORTED;
     if ((long long)c->max_pages * c->page > kMaxInt || (long long)c->B * c->H_kv > kMaxInt)
         return FA_ERR_INVALID_ARGUMENT;
+    // (page, head, 16 tokens) units of the pool are counted in 32 bits
+    if ((long long)c->n_pages * c->H_kv > kMaxInt / (c->page / 16)) return FA_ERR_INVALID_ARGUMENT;
     if (c->B == 0 || c->H_kv == 0) return FA_OK;
     if (c->n_pages > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)) return FA_ERR_INVALID_ARGUMENT;
     if (c->max_pages > 0 && !c->table) return FA_ERR_INVALID_ARGUMENT;
@@ -82,7 +84,12 @@ struct AttnPlan {
 };
 
 // CTAs that one SM holds (the kernel's launch bounds).
-int attn_occupancy(int d, int nt) { return d == 256 ? 2 : (nt == 2 ? 3 : 4); }
+int attn_resident(int d, int nt) {
+    namespace ca = fa::cattn;
+    if (d == 64) return nt == 1 ? ca::kResident<64, 1> : ca::kResident<64, 2>;
+    if (d == 128) return nt == 1 ? ca::kResident<128, 1> : ca::kResident<128, 2>;
+    return ca::kResident<256, 1>;
+}
 
 AttnPlan plan_attn(const fa_cache_attn_params *p, int resident) {
     namespace ca = fa::cattn;
@@ -93,8 +100,7 @@ AttnPlan plan_attn(const fa_cache_attn_params *p, int resident) {
     a.chunks = (a.rows + 8 * a.nt - 1) / (8 * a.nt);
     long long w = resident / a.chunks;
     const long long tiles = (long long)c.B * c.H_kv * (((long long)c.max_pages * c.page) / ca::kTile);
-    const long long most = (tiles + ca::kWarps - 1) / ca::kWarps;  // a worker takes a tile for each warp at least
-    if (w > most) w = most;
+    if (w > tiles) w = tiles;  // a worker takes one at least
     a.workers = w < 1 ? 1 : (int)w;
     const size_t slots = (size_t)a.chunks * a.workers * 2 * 8 * a.nt;
     a.o_bytes = slots * c.d * sizeof(float);
@@ -106,8 +112,25 @@ bool attn_empty(const fa_cache_attn_params *p) {
     return p->cache.B == 0 || p->cache.H_kv == 0 || p->H == 0 || p->N == 0;
 }
 
+template <int D, int WPR>
+fa_status launch_merge(const fa::cattn::Params &kp, int nt8, cudaStream_t s) {
+    constexpr int warps = fa::cattn::kMergeWarps<WPR>, per_cta = warps / WPR;
+    const long long rows = (long long)kp.c.B * kp.c.H_kv * kp.rows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((rows + per_cta - 1) / per_cta));
+    cfg.blockDim = dim3(32 * warps);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa::cattn::fa_cache_merge_kernel<D, WPR>, kp, nt8) == cudaSuccess ? FA_OK
+                                                                                                       : FA_ERR_CUDA;
+}
+
 template <int D, int NT>
-fa_status launch_attn(const fa::cattn::Params &kp, int dev, cudaStream_t s) {
+fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_t s) {
     namespace ca = fa::cattn;
     static std::atomic<bool> ready[kMaxDevices];
     auto kern = ca::fa_cache_attn_kernel<D, NT>;
@@ -116,25 +139,18 @@ fa_status launch_attn(const fa::cattn::Params &kp, int dev, cudaStream_t s) {
             return FA_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }
-    kern<<<kp.chunks * kp.workers, ca::kThreads, ca::kSmemBytes<D>, s>>>(kp);
+    // few workers are spread over the SMs, one warp in a CTA at work
+    const int warps = kp.chunks * kp.workers, ctas = ca::kResident<D, NT> * sms;
+    const int full = (warps + ca::kWarps - 1) / ca::kWarps;
+    kern<<<full > ctas ? full : (warps < ctas ? warps : ctas), ca::kThreads, ca::kSmemBytes<D>, s>>>(kp);
     if (cudaPeekAtLastError() != cudaSuccess) return FA_ERR_CUDA;
 
-    // The merge is launched while the first kernel runs and waits in it for its results.
-    // One warp for a row, or eight where few (sequence, head) pairs mean many parts each.
-    const long long rows = (long long)kp.c.B * kp.c.H_kv * kp.rows;
-    const bool wide = kp.workers > 8LL * kp.c.B * kp.c.H_kv;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + ca::kMergeWarps - 1) / ca::kMergeWarps));
-    cfg.blockDim = dim3(32 * ca::kMergeWarps);
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, ca::fa_cache_merge_kernel<D, ca::kMergeWarps>, kp, 8 * NT)
-                               : cudaLaunchKernelEx(&cfg, ca::fa_cache_merge_kernel<D, 1>, kp, 8 * NT);
-    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    // The merge is launched while the first kernel runs and waits in it for its results.  A pair
+    // has about workers / pairs parts: one warp for a row, or more where there are many.
+    const long long pairs = (long long)kp.c.B * kp.c.H_kv;
+    if (kp.workers <= 4 * pairs) return launch_merge<D, 1>(kp, 8 * NT, s);
+    if (kp.workers <= 64 * pairs) return launch_merge<D, 8>(kp, 8 * NT, s);
+    return launch_merge<D, 32>(kp, 8 * NT, s);
 }
 
 }  // namespace
@@ -234,8 +250,12 @@ fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream) {
     if ((p->causal != 0 && p->causal != 1) || !std::isfinite(p->scale) || p->scale <= 0.f)
         return FA_ERR_INVALID_ARGUMENT;
     if (p->o_dtype != FA_O_F32 && p->o_dtype != FA_O_BF16) return FA_ERR_INVALID_ARGUMENT;
+    if (p->test_drop_load < 0) return FA_ERR_INVALID_ARGUMENT;
     if (attn_empty(p)) return FA_OK;
     if (p->H % c.H_kv != 0 || (long long)c.B * p->H > kMaxInt / p->N) return FA_ERR_INVALID_ARGUMENT;
+    // the kernels' line of (sequence, head) pairs is counted in 32 bits
+    if ((long long)c.B * c.H_kv > kMaxInt / ((long long)c.max_pages * (c.page / fa::cattn::kTile) + fa::cattn::kPairCost))
+        return FA_ERR_INVALID_ARGUMENT;
     if (!p->q || !p->o || !p->lse || !p->k_len || !p->workspace) return FA_ERR_INVALID_ARGUMENT;
     if (!aligned(p->q, 16) || !aligned(p->o, 16) || !aligned(p->workspace, 16) || !aligned(p->lse, 4) ||
         !aligned(p->k_len, 4) || !aligned(p->dev_status, 4))
@@ -245,7 +265,7 @@ fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream) {
     if ((st = fa_detail::current_device(&dev, &sms)) != FA_OK) return st;
 
     AttnPlan a = plan_attn(p, fa::cattn::kMaxWorkers);
-    const int resident = attn_occupancy(c.d, a.nt) * sms;
+    const int resident = attn_resident(c.d, a.nt) * fa::cattn::kWarps * sms;  // warps
     if (resident < fa::cattn::kMaxWorkers) a = plan_attn(p, resident);
     fa::cattn::Params kp;
     std::memset(&kp, 0, sizeof kp);
@@ -264,11 +284,20 @@ fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream) {
     kp.causal = p->causal;
     kp.o_bf16 = p->o_dtype == FA_O_BF16;
     kp.scale_log2 = (float)((double)p->scale * 1.4426950408889634074);
+    kp.timeout_ns = (uint64_t)(p->timeout_ms ? p->timeout_ms : 2000u) * 1000000ull;
+    kp.drop_load = p->test_drop_load;
+    // without any page there is nothing to copy; the map only has to be a valid one
+    const bool pages = c.n_pages > 0;
+    const int line = c.d == 256 ? 256 : 128, lines = fa::cattn::kTile * c.d / line;
+    const long long tiles = pages ? (long long)c.n_pages * c.H_kv * (c.page / fa::cattn::kTile) : 1;
+    if ((st = fa_detail::encode_cache_map(&kp.tm_k, pages ? c.k : p->workspace, tiles, lines, line)) != FA_OK ||
+        (st = fa_detail::encode_cache_map(&kp.tm_v, pages ? c.v : p->workspace, tiles, lines, line)) != FA_OK)
+        return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (c.d) {
-        case 64: return a.nt == 1 ? launch_attn<64, 1>(kp, dev, s) : launch_attn<64, 2>(kp, dev, s);
-        case 128: return a.nt == 1 ? launch_attn<128, 1>(kp, dev, s) : launch_attn<128, 2>(kp, dev, s);
-        default: return launch_attn<256, 1>(kp, dev, s);
+        case 64: return a.nt == 1 ? launch_attn<64, 1>(kp, dev, sms, s) : launch_attn<64, 2>(kp, dev, sms, s);
+        case 128: return a.nt == 1 ? launch_attn<128, 1>(kp, dev, sms, s) : launch_attn<128, 2>(kp, dev, sms, s);
+        default: return launch_attn<256, 1>(kp, dev, sms, s);
     }
 }
 

@@ -15,17 +15,21 @@
 // O^T = V^T P^T are computed transposed (mma m16n8k16, tokens or components
 // on the 16 side, query rows on the 8 side), so that the 4 to 8 query rows
 // that share a key fill the tensor core's narrow side and the codes are the
-// A operand.  Which token or component a matrix row stands for is free, and it is
-// chosen such that each lane's operands are whole 16-byte runs (8 for the values of
-// d = 64) of the cache: every lane copies, by cp.async, what it will itself read, into
-// its own slots of a ring in shared memory.  That needs no barrier, has no bank
-// conflicts, and keeps the copies in flight out of the registers.
-// tcgen05 would want 128 rows: at 8 rows 15/16 of it would be idle, and the codes would have to be
-// written back to shared memory as fp16 for it.
+// A operand.  tcgen05 would want 128 rows: at 8 rows 15/16 of it would be idle, and the
+// codes would have to go back to shared memory as fp16 for it.
+// Every warp works by itself: it has a ring of tiles that TMA fills (one lane issues),
+// with an mbarrier for each, and no barrier is shared between warps.  Which token
+// or component a row of a matrix stands for is free; it is chosen such that a
+// lane reads its operands from the 128-byte-swizzled tile as whole 16-byte runs (8 for
+// the values of d = 64) without bank conflicts: row r of K is token tau(r) (8 + tau(r - 8)).
 //
-// Bound by memory: 2 d bytes per token and key/value head, read once for
-// all query rows that share it.
+// Bound by memory: 2 d bytes per token and key/value head, read once for all
+// query rows that share it.  The same tiles fetched by 16-byte cp.async (64 bytes
+// of a key for each group of 4 lanes) stopped at 4.8 TB/s whatever was done with
+// them; TMA's requests reach the copy rate.
 #pragma once
+
+#include <cuda.h>
 
 #include <cstdint>
 
@@ -38,16 +42,34 @@ namespace cattn {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;         // tokens a warp takes at a time; divides every page size
-constexpr int kMaxWorkers = 640;  // CTAs that take work, at most
+constexpr int kMaxWorkers = 2560;  // warps that take work, at most
+// What a warp spends on a (sequence, head) pair besides its tiles (the table, the queries, the
+// first copies, the result), in tiles.
+constexpr int kPairCost = 6;
+constexpr int kMinRun = 4;        // of one worker, in tiles
 
-template <int D> constexpr int kStages = D == 64 ? 4 : (D == 128 ? 3 : 2);
+// Tiles of one step (two: their chains of products and the softmax's reductions overlap)
+// and of the ring.
+template <int D> constexpr int kStep = D == 64 ? 2 : 1;
+template <int D> constexpr int kStages = D == 64 ? 4 : 3;
+// CTAs for each SM.  More tiles in flight are not better: d = 128 with one CTA more or a tile
+// more in the ring took 5 to 15 % longer.
+template <int D, int NT> constexpr int kResident = D == 64 ? (NT == 2 ? 3 : 4) : (D == 128 ? 3 : 2);
 template <int D> constexpr int kStageBytes = 2 * kTile * D;  // codes of K and V
 template <int D> constexpr int kRingBytes = kStages<D> * kStageBytes<D>;
-template <int D> constexpr int kSmemBytes = kWarps * kRingBytes<D>;
+template <int D> constexpr int kSmemBytes = kWarps * kRingBytes<D> + 1024;  // the rings begin on a swizzle atom
+// tau: three bits for each of 8 rows, every fourth bit left out.  d = 64 has two tokens in a
+// 128-byte line, the others one (or half of one).
+template <int D> constexpr uint32_t kTau = D == 64 ? 0x65217430u : 0x37621540u;
+template <int D>
+__device__ __forceinline__ int tau(int r) { return (kTau<D> >> (4 * r)) & 7; }
+// Byte b of a tile of 128-byte lines under the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(uint32_t b) { return b ^ (((b >> 7) & 7) << 4); }
 // query rows one CTA handles: 8 NT
 template <int D> constexpr int kMaxNT = D == 256 ? 1 : 2;
 
 struct Params {
+    CUtensorMap tm_k, tm_v;  // codes as [tiles][16 d / line][line], line = 128 bytes (256 for d = 256), swizzled
     CacheView c;
     const uint16_t *q;
     void *o;
@@ -57,9 +79,11 @@ struct Params {
     float *o_part;        // [chunk][worker][2][8 NT][D]
     float2 *ml_part;      // [chunk][worker][2][8 NT] (m, l)
     int N, rows;          // query tokens; rows that share a key/value head: group * N
-    int chunks, workers;  // blocks of 8 NT rows; CTAs for each of them
+    int chunks, workers;  // blocks of 8 NT rows; warps for each of them
     int causal, o_bf16;
     float scale_log2;
+    uint64_t timeout_ns;
+    int drop_load;        // test: the first warp never issues its n-th tile
 };
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -71,63 +95,62 @@ __device__ __forceinline__ int seq_len(const Params &p, int b) {
 }
 __device__ __forceinline__ int seq_tiles(const Params &p, int b) { return (seq_len(p, b) + kTile - 1) / kTile; }
 
-// The plan: the tiles of all (sequence, key/value head) pairs, in that order, are
-// cut into runs of `per` tiles, one for each worker.  At least one tile for each
-// warp; a multiple of the warps where a run is short enough for it to matter.
-struct Plan {
-    long long total;
-    long long per;
-};
-__device__ __forceinline__ Plan make_plan(const Params &p) {
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l == 0.f ? neg_inf() : ((m == neg_inf() ? 0.f : m) + log2f(l)) * 0.693147180559945f;
+}
+
+// The plan: all (sequence, key/value head) pairs with tiles, in that order, lie on a line,
+// each kPairCost + its tiles long, and the line is cut into runs of `per`, one
+// for each worker (kMinRun at least).  Its length is below 2^31.
+__device__ __forceinline__ int pair_cost(int tiles) { return tiles ? tiles + kPairCost : 0; }
+
+// Lanes' lengths on the line of sequences b0 .. b0 + 31, and their running sum.
+__device__ __forceinline__ void scan_costs(const Params &p, int b0, int &own, int &sum) {
     const int lane = threadIdx.x & 31;
-    long long t = 0;
-    for (int b = lane; b < p.c.B; b += 32) t += seq_tiles(p, b);
+    own = b0 + lane < p.c.B ? pair_cost(seq_tiles(p, b0 + lane)) * p.c.H_kv : 0;
+    sum = own;
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) t += __shfl_xor_sync(0xffffffffu, t, i);
+    for (int i = 1; i < 32; i <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, i);
+        if (lane >= i) sum += o;
+    }
+}
+
+struct Plan {
+    int total, per;
+    int own, sum;  // scan_costs of the first 32 sequences
+};
+template <int D>
+__device__ __forceinline__ Plan make_plan(const Params &p) {
     Plan r;
-    r.total = t * p.c.H_kv;
-    r.per = (r.total + p.workers - 1) / p.workers;
-    if (r.per < 16 * kWarps) r.per = (r.per + kWarps - 1) / kWarps * kWarps;
-    if (r.per < kWarps) r.per = kWarps;
+    scan_costs(p, 0, r.own, r.sum);
+    r.total = __shfl_sync(0xffffffffu, r.sum, 31);
+    for (int b0 = 32; b0 < p.c.B; b0 += 32) {
+        const int b = b0 + (threadIdx.x & 31);
+        const int own = b < p.c.B ? pair_cost(seq_tiles(p, b)) * p.c.H_kv : 0;
+        r.total += __reduce_add_sync(0xffffffffu, own);
+    }
+    r.per = max((int)(((unsigned)r.total + p.workers - 1) / (unsigned)p.workers), kMinRun);
     return r;
 }
 
-// The sequence that holds tile g < total, and its first tile.
-__device__ __forceinline__ void locate(const Params &p, long long g, int &b, long long &first) {
-    const int lane = threadIdx.x & 31;
-    long long before = 0;
-    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-        const long long own = b0 + lane < p.c.B ? (long long)seq_tiles(p, b0 + lane) * p.c.H_kv : 0;
-        long long inc = own;
-#pragma unroll
-        for (int i = 1; i < 32; i <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, inc, i);
-            if (lane >= i) inc += o;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + inc > g);
+// The sequence that holds place x < total of the line, and where it begins.
+__device__ __forceinline__ void locate(const Params &p, const Plan &plan, int x, int &b, int &first) {
+    int before = 0, own = plan.own, sum = plan.sum;
+    for (b = 0;; b += 32) {
+        const unsigned hit = __ballot_sync(0xffffffffu, before + sum > x);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            b = b0 + l;
-            first = before + __shfl_sync(0xffffffffu, inc - own, l);
+            b += l;
+            first = before + __shfl_sync(0xffffffffu, sum - own, l);
             return;
         }
-        before += __shfl_sync(0xffffffffu, inc, 31);
+        before += __shfl_sync(0xffffffffu, sum, 31);
+        scan_costs(p, b + 32, own, sum);
+        if (b + 32 >= p.c.B) return;  // (x < total: not reached)
     }
-    b = p.c.B;
-    first = before;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void *src, bool take) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(take ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 r;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
@@ -181,109 +204,136 @@ __device__ __forceinline__ void v_operands(uint32_t (&a)[2][4], const VWords<D> 
 
 __device__ __forceinline__ bool has_nan_code(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// One CTA: a run of tiles, segment by segment ((sequence, head) pairs).  The
-// warps of the CTA take a segment's tiles in turn and merge at its end.
+// One warp: a run of the line, pair by pair.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : (NT == 2 ? 3 : 4))
+__global__ void __launch_bounds__(kThreads, kResident<D, NT>)
 fa_cache_attn_kernel(const __grid_constant__ Params p) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 s_ml[kWarps][8 * NT];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_bar[kWarps][kStages<D>];
+    __shared__ int s_abort[kWarps];
     constexpr int KJ = D / 64;               // 16-byte runs of a key for each lane
-    constexpr int RS = D + 4;                // row stride of the merge's floats
-    static_assert(8 * NT * RS * 4 <= kRingBytes<D>, "the merge's rows lie in the warp's ring");
+    constexpr int T = kStep<D>, S = kStages<D>;
+    constexpr int CH = T == 1 ? 2 : 1;       // sums that a tile's scores are split into
+    static_assert(S % T == 0 && 32 % T == 0, "steps do not straddle the ring's end or a window's");
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&p.tm_k);
+        prefetch_tensormap(&p.tm_v);
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    const int chunk = blockIdx.x % p.chunks, worker = blockIdx.x / p.chunks;
+    // neighbours on the line are on different SMs: few workers still use them all
+    const int id = warp * gridDim.x + blockIdx.x;
+    if (id >= p.chunks * p.workers) return;
+    const int chunk = id % p.chunks, worker = id / p.chunks;
     const int row0 = chunk * 8 * NT;
-    const Plan plan = make_plan(p);
-    long long at = worker * plan.per;
-    const long long end = min(plan.total, at + plan.per);
-    if (at >= end) return;
-    int b;
-    long long first;
-    locate(p, at, b, first);
+    const Plan plan = make_plan<D>(p);
+    if ((long long)worker * plan.per >= plan.total) return;
+    int at = worker * plan.per;
+    const int end = at + min(plan.total - at, plan.per);
+    int b, first;
+    locate(p, plan, at, b, first);
 
-    uint8_t *ring = smem + warp * kRingBytes<D>;
-    const uint32_t ring_u32 = smem_u32(ring);
-    const uint32_t k_slot = ring_u32 + 16 * lane;
-    const uint32_t v_slot = ring_u32 + kTile * D + (D == 64 ? 8 : 16) * lane;
-    const int tile_shift = p.c.page_log2 - 4;
+    const uint32_t ring = ((smem_u32(smem_raw) + 1023) & ~1023u) + warp * kRingBytes<D>;
+    uint64_t *bar = s_bar[warp];
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(&bar[i], 2);  // K and V of a tile
+        fence_mbar_init();
+        s_abort[warp] = 0;
+    }
+    __syncwarp();
     const CacheView &cv = p.c;
+    // this lane's places in a tile: runs j and j + 1 (d >= 128) of key tau(g) (+ 8 tokens: + 8 d
+    // bytes, for d = 64 in the other half of the line's chunks), and of values tau(2c), tau(2c + 1)
+    const uint32_t k_at = ring + swizzled(tau<D>(g) * (D == 64 ? 64 : 128) + 16 * c);
+    const uint32_t v_at0 = ring + kTile * D + swizzled(tau<D>(2 * c) * (D == 64 ? 64 : 128) + (D == 64 ? 8 : 16) * g);
+    const uint32_t v_at1 = ring + kTile * D + swizzled(tau<D>(2 * c + 1) * (D == 64 ? 64 : 128) + (D == 64 ? 8 : 16) * g);
+    const int tile_shift = cv.page_log2 - 4;
+    int slot0 = 0;        // slot of the next step's first tile, and the parity of its phase
+    uint32_t parity = 0;
 
-    while (at < end) {
-        const int len = seq_len(p, b);
-        const int nb = (len + kTile - 1) / kTile;
-        if (at - first >= (long long)nb * cv.H_kv) {  // next sequence (this one may be empty)
-            first += (long long)nb * cv.H_kv;
-            ++b;
-            continue;
-        }
-        const int h = (int)((at - first) / nb);
-        const int t0 = (int)(at - first - (long long)h * nb);
-        const int t1 = (int)min((long long)nb, t0 + (end - at));
-        at += t1 - t0;
-        const long long q_row = ((long long)b * cv.H_kv + h) * p.rows + row0;  // first row of q, o, lse
-        const int32_t *table = cv.table + b * cv.table_stride;
-
-        // ---- this warp's tiles: t0 + warp + 4 i, i < n_own
-        const int n_own = (t1 - t0 - warp + kWarps - 1) / kWarps;
-        // windows of 32 own tiles: lane i has tile i's page and scales
-        int w_page = -1;
-        float w_ks = -1.f, w_vs = 0.f, w_ks_old = -1.f, w_vs_old = 0.f;
-        auto load = [&](int i) {  // own tile i into its stage
-            if ((i & 31) == 0) {
-                w_ks_old = w_ks;
-                w_vs_old = w_vs;
-                w_page = -1;
-                w_ks = -1.f;  // marks a page outside the pool
-                w_vs = 0.f;
-                if (i + lane < n_own) {
-                    const int t = t0 + warp + kWarps * (i + lane);
-                    const int page_id = __ldg(table + (t >> tile_shift));
-                    if (page_id >= 0 && page_id < cv.n_pages) {
-                        w_page = page_id;
-                        const long long unit = (long long)page_id * cv.H_kv + h;
-                        w_ks = cv.k_scale[unit];
-                        w_vs = cv.v_scale[unit];
-                    } else {
-                        report_bad_page(p.status);
-                    }
-                }
+    // The pair at hand: its first row of q, o and lse, its tokens, its page table, and the tiles
+    // t0 .. t0 + n_own of its nb that are this warp's.
+    long long q_row = 0;
+    const int32_t *table = nullptr;
+    int len = 0, nb = 0, h = 0, t0 = 0, n_own = 0, n_pad = 0;
+    // windows of 32 own tiles: lane i has tile i's place in the pool (in tiles) and scales;
+    // the copies run ahead of the products, so the window before is kept
+    int w_tile = -1;
+    float w_ks = -1.f, w_lv = 0.f, w_ks_old = -1.f, w_lv_old = 0.f;
+    auto window = [&](int i) {
+        w_ks_old = w_ks;
+        w_lv_old = w_lv;
+        w_tile = -1;
+        w_ks = -1.f;  // marks a page outside the pool
+        w_lv = 0.f;
+        if (i + lane < n_own) {
+            const int t = t0 + i + lane;
+            const int page_id = __ldg(table + (t >> tile_shift));
+            if (page_id >= 0 && page_id < cv.n_pages) {
+                const int unit = page_id * cv.H_kv + h;
+                w_tile = (unit << tile_shift) + (t & ((1 << tile_shift) - 1));
+                w_ks = cv.k_scale[unit];
+                w_lv = __log2f(cv.v_scale[unit]);
+            } else {
+                report_bad_page(p.status);
             }
-            const int page_id = __shfl_sync(0xffffffffu, w_page, i & 31);
-            const int t = t0 + warp + kWarps * i;
-            const int slot = (t & ((1 << tile_shift) - 1)) * kTile;
-            const int left = page_id < 0 ? 0 : len - t * kTile;  // tokens of the tile to read
-            const long long off = (((long long)max(page_id, 0) * cv.H_kv + h) * cv.page + slot) * D;
-            const uint32_t st = (uint32_t)(i % kStages<D>) * kStageBytes<D>;
-            const uint8_t *ks = cv.k + off + g * D + 16 * c;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int j = 0; j < KJ; ++j)
-                    cp16(k_slot + st + (r * KJ + j) * 512, ks + r * 8 * D + 64 * j, g + 8 * r < left);
-            const uint8_t *vs = cv.v + off + 2 * c * D + (D == 64 ? 8 : 16) * g;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int tok = (r & 1) + 8 * (r >> 1);
-                const bool take = 2 * c + tok < left;
-                if constexpr (D == 64) {
-                    cp8(v_slot + st + r * 256, vs + tok * D, take);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < D / 128; ++j)
-                        cp16(v_slot + st + (r * (D / 128) + j) * 512, vs + tok * D + 128 * j, take);
-                }
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < kStages<D> - 1; ++i) {
-            if (i < n_own) load(i);
-            cp_commit();
         }
+    };
+    // Copies of own tile i into the slot at `st`.  A page outside the pool, and the place of a
+    // missing second tile of the last step, have nothing to copy: their phase
+    // completes all the same.
+    auto load = [&](int i, int slot, bool keys) {
+        const int tile = __shfl_sync(0xffffffffu, w_tile, i & 31);
+        if (lane == 0) {
+            if (tile < 0) {
+                mbar_arrive(&bar[slot]);
+            } else if (p.drop_load <= 0 || i != p.drop_load - 1 || id != 0) {
+                const uint32_t dst = ring + slot * kStageBytes<D> + (keys ? 0 : kTile * D);
+                const CUtensorMap *map = keys ? &p.tm_k : &p.tm_v;
+                mbar_arrive_expect_tx(&bar[slot], kTile * D);
+                tma_load_3d_at(dst, map, &bar[slot], 0, 0, tile);
+                if constexpr (D == 256) tma_load_3d_at(dst + kTile * 128, map, &bar[slot], 128, 0, tile);
+            }
+        }
+    };
+    // Takes the next pair of the run and starts its copies; false at the run's end.
+    auto next_pair = [&]() -> bool {
+        while (at < end) {
+            len = seq_len(p, b);
+            nb = (len + kTile - 1) / kTile;
+            const int cost = pair_cost(nb);
+            if (at - first >= cost * cv.H_kv) {  // next sequence (this one may be empty)
+                first += cost * cv.H_kv;
+                ++b;
+                continue;
+            }
+            h = (at - first) / cost;
+            const int from = at - first - h * cost;
+            const int to = min(cost, from + (end - at));
+            at += to - from;
+            t0 = max(from - kPairCost, 0);
+            n_own = max(to - kPairCost, 0) - t0;
+            if (n_own > 0) break;  // else the run has none of the pair's tiles, only its begin
+        }
+        if (n_own <= 0) return false;
+        n_pad = (n_own + T - 1) / T * T;
+        q_row = ((long long)b * cv.H_kv + h) * p.rows + row0;
+        table = cv.table + b * cv.table_stride;
+        window(0);
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            if (i < n_pad) {
+                const int slot = slot0 + i < S ? slot0 + i : slot0 + i - S;
+                load(i, slot, true);
+                load(i, slot, false);
+            }
+        return true;
+    };
 
+    bool more = next_pair();
+    while (more) {
         // ---- queries: fp16 of each row times a power of two that brings its
         // largest magnitude to [2^14, 2^15); bf16's 8 bits stay exact but for
         // components 2^-29 below the row's largest
@@ -341,94 +391,141 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
 
         float acc[NT][D / 16][4];
         float m[NT][2], n[NT][2], l[NT][2];
+        float m0[NT][2], n0[NT][2];  // what is added to a score: -m, and 7 - n (0 and 7 while nothing is seen)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) m[t][i] = n[t][i] = neg_inf(), l[t][i] = 0.f;
+            for (int i = 0; i < 2; ++i) {
+                m[t][i] = n[t][i] = neg_inf();
+                l[t][i] = m0[t][i] = 0.f;
+                n0[t][i] = 7.f;
+            }
         }
 
-        for (int i = 0; i < n_own; ++i) {
-            if (i + kStages<D> - 1 < n_own) load(i + kStages<D> - 1);
-            cp_commit();
-            cp_wait<kStages<D> - 1>();
-            const uint32_t st = (uint32_t)(i % kStages<D>) * kStageBytes<D>;
-            const int tok0 = (t0 + warp + kWarps * i) * kTile;
-            const bool old = (min(i + kStages<D> - 1, n_own - 1) >> 5) != (i >> 5);  // its window has been left
-            const float ks = __shfl_sync(0xffffffffu, old ? w_ks_old : w_ks, i & 31);
-            const float vs = __shfl_sync(0xffffffffu, old ? w_vs_old : w_vs, i & 31);
-            const float lv = __log2f(vs);
-
-            // ---- S^T, in two sums
-            float s[NT][2][4];
+        bool failed = false;
+        for (int i = 0; i < n_own; i += T) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s[t][0][k] = s[t][1][k] = 0.f;
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) {
-                const uint4 a = lds16(k_slot + st + j * 512), bq = lds16(k_slot + st + (KJ + j) * 512);
-                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {bq.x, bq.y, bq.z, bq.w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t a0, a1, a2, a3;
-                    half4(aw[w], a0, a2);
-                    half4(bw[w], a1, a3);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        mma16816(s[t][w & 1], a0, a1, a2, a3, qf[t][4 * j + w][0], qf[t][4 * j + w][1]);
-                }
-            }
-            VWords<D> v;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if constexpr (D == 64) {
-                    const uint2 x = lds8(v_slot + st + r * 256);
-                    v[r][0] = x.x;
-                    v[r][1] = x.y;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < D / 128; ++j) {
-                        const uint4 x = lds16(v_slot + st + (r * (D / 128) + j) * 512);
-                        v[r][4 * j] = x.x;
-                        v[r][4 * j + 1] = x.y;
-                        v[r][4 * j + 2] = x.z;
-                        v[r][4 * j + 3] = x.w;
+            for (int u = 0; u < T; ++u)
+                if (!failed && !mbar_wait(&bar[slot0 + u], parity, &s_abort[warp], p.timeout_ns)) failed = true;
+            failed = __any_sync(0xffffffffu, failed);
+            if (failed) {
+                // The copies in flight end (or their waits run out) before the ring is used otherwise.
+                for (int k = i; k < min(i + S, n_pad); ++k) {
+                    const int at_k = slot0 + (k - i);
+                    const uint64_t since = globaltimer_ns();
+                    while (!mbar_try_wait(smem_u32(&bar[at_k % S]), parity ^ (at_k >= S)) &&
+                           globaltimer_ns() - since < p.timeout_ns) {
                     }
                 }
+                if (lane == 0 && p.status) atomicCAS(p.status, 0, (int)FA_ERR_DEVICE_TIMEOUT);
+                break;
+            }
+            const uint32_t st = slot0 * kStageBytes<D>;
+            // the copies have reached tile i + S - 1: its window is the current one
+            const bool old = (min(i + S, n_pad) - 1) >> 5 != i >> 5;
+            float ks[T], lv[T];
+            bool bad[T], edge[T];
+            int tok0[T];
+#pragma unroll
+            for (int u = 0; u < T; ++u) {
+                ks[u] = __shfl_sync(0xffffffffu, old ? w_ks_old : w_ks, (i + u) & 31);
+                lv[u] = __shfl_sync(0xffffffffu, old ? w_lv_old : w_lv, (i + u) & 31);
+                tok0[u] = (t0 + i + u) * kTile;
+                bad[u] = i + u >= n_own || ks[u] < 0.f;
+                edge[u] = tok0[u] + kTile > all || bad[u];
             }
 
-            // ---- scores in units of log2; x[t][0..1] token g, x[t][2..3] token g + 8
-            float x[NT][4];
-            const bool bad = ks < 0.f;
-            const bool edge = tok0 + kTile > all || bad;
+            // ---- S^T
+            float s[T][NT][CH][4];
+#pragma unroll
+            for (int u = 0; u < T; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int x = 0; x < CH; ++x) s[u][t][x][k] = 0.f;
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                uint4 ka[T], kb[T];
+#pragma unroll
+                for (int u = 0; u < T; ++u) {
+                    // run j: for d >= 128 chunk c + 4 (j & 1) of the line, in half j / 2 of the tile
+                    const uint32_t at_k = k_at + st + u * kStageBytes<D> + (j >> 1) * (kTile * 128);
+                    ka[u] = lds16(at_k ^ ((j & 1) * 64));
+                    kb[u] = D == 64 ? lds16((at_k + 512) ^ 64) : lds16((at_k + 1024) ^ ((j & 1) * 64));
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int u = 0; u < T; ++u) {
+                        const uint32_t aw[4] = {ka[u].x, ka[u].y, ka[u].z, ka[u].w};
+                        const uint32_t bw[4] = {kb[u].x, kb[u].y, kb[u].z, kb[u].w};
+                        uint32_t a0, a1, a2, a3;
+                        half4(aw[w], a0, a2);
+                        half4(bw[w], a1, a3);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            mma16816(s[u][t][w % CH], a0, a1, a2, a3, qf[t][4 * j + w][0], qf[t][4 * j + w][1]);
+                    }
+            }
+            // the keys' slots are free: every lane's reads were operands of the products above
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < T; ++u)
+                if (i + u + S < n_pad) {
+                    if (((i + u + S) & 31) == 0) window(i + u + S);
+                    load(i + u + S, slot0 + u, true);
+                }
+
+            // ---- scores in units of log2; x[..][0..1] token tau(g), x[..][2..3] token tau(g) + 8
+            float x[T][NT][4];
             bool raise = false;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float f[2] = {rs[t][0] * ks, rs[t][1] * ks};
+            for (int u = 0; u < T; ++u)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[t][k] = (s[t][0][k] + s[t][1][k]) * f[k & 1];
-                    if (edge && (bad || tok0 + g + 8 * (k >> 1) >= lim[t][k & 1])) x[t][k] = neg_inf();
-                    raise |= x[t][k] > m[t][k & 1] + 8.f || x[t][k] + lv > n[t][k & 1] + 8.f;
+                for (int t = 0; t < NT; ++t) {
+                    const float f[2] = {rs[t][0] * ks[u], rs[t][1] * ks[u]};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float y = s[u][t][0][k];
+                        if constexpr (CH == 2) y += s[u][t][1][k];
+                        x[u][t][k] = y * f[k & 1];
+                    }
+                    if (edge[u]) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (bad[u] || tok0[u] + tau<D>(g) + 8 * (k >> 1) >= lim[t][k & 1]) x[u][t][k] = neg_inf();
+                    }
+                    // n - lv is +inf for a scale of 0 (and NaN, which fminf leaves out, if nothing is seen)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        raise |= fmaxf(x[u][t][k], x[u][t][k + 2]) > fminf(m[t][k], n[t][k] - lv[u]) + 8.f;
                 }
-            }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float top = fmaxf(x[t][k], x[t][k + 2]);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float mn = fmaxf(m[t][k], top), nn = fmaxf(n[t][k], top + lv);
+                        float mn = m[t][k], nn = n[t][k];
+#pragma unroll
+                        for (int u = 0; u < T; ++u) {
+                            float top = fmaxf(x[u][t][k], x[u][t][k + 2]);
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                            mn = fmaxf(mn, top);
+                            nn = fmaxf(nn, top + lv[u]);
+                        }
                         // nothing seen yet (-inf): there is nothing to rescale
                         const float fl = m[t][k] == neg_inf() ? 1.f : ex2_approx(m[t][k] - mn);
                         const float fa = n[t][k] == neg_inf() ? 1.f : ex2_approx(n[t][k] - nn);
                         m[t][k] = mn;
                         n[t][k] = nn;
+                        m0[t][k] = mn == neg_inf() ? 0.f : -mn;
+                        n0[t][k] = nn == neg_inf() ? 7.f : 7.f - nn;
                         l[t][k] *= fl;
 #pragma unroll
                         for (int d = 0; d < D / 16; ++d) {
@@ -437,73 +534,115 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                         }
                     }
             }
-            uint32_t pb[NT][2];
+            uint32_t pb[T][NT][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float w[4];
+            for (int u = 0; u < T; ++u)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float mr = m[t][k & 1], nr = n[t][k & 1];
-                    l[t][k & 1] += ex2_approx(x[t][k] - (mr == neg_inf() ? 0.f : mr));
-                    w[k] = ex2_approx(x[t][k] + (lv - (nr == neg_inf() ? 0.f : nr) + 7.f));
+                for (int t = 0; t < NT; ++t) {
+                    float w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        l[t][k & 1] += ex2_approx(x[u][t][k] + m0[t][k & 1]);
+                        w[k] = ex2_approx(x[u][t][k] + (lv[u] + n0[t][k & 1]));
+                    }
+                    pb[u][t][0] = transposed8x8(pack_half2(w[0], w[1]));
+                    pb[u][t][1] = transposed8x8(pack_half2(w[2], w[3]));
                 }
-                pb[t][0] = transposed8x8(pack_half2(w[0], w[1]));
-                pb[t][1] = transposed8x8(pack_half2(w[2], w[3]));
-            }
 
-            // ---- O^T.  A NaN code among tokens that some rows do not see must not
-            // reach those rows (0 * NaN): then the product is taken for each query
-            // token by itself, with only the values that it sees.
-            bool special = false;
-            if (edge && p.causal && p.N > 1) {
+            // ---- O^T
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+            for (int u = 0; u < T; ++u) {
+                // nothing to add, and nothing was copied (a missing tile is the step's last)
+                if (!bad[u]) {
+                    const uint32_t st_v = st + u * kStageBytes<D>;
+                    VWords<D> v;
 #pragma unroll
-                    for (int w = 0; w < D / 32; ++w) special |= has_nan_code(v[r][w]);
-            }
-            if (edge && __any_sync(0xffffffffu, special)) {
-                for (int tq = 0; tq < p.N; ++tq) {
-                    const int seen = len - p.N + tq + 1 - tok0;
-                    VWords<D> vm;
+                    for (int r = 0; r < 4; ++r) {
+                        // token tau(2c + r % 2) + 8 (r / 2)
+                        const uint32_t at_v = ((r & 1) ? v_at1 : v_at0) + st_v;
+                        if constexpr (D == 64) {
+                            const uint2 y = lds8(r < 2 ? at_v : (at_v + 512) ^ 64);
+                            v[r][0] = y.x;
+                            v[r][1] = y.y;
+                        } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int w = 0; w < D / 32; ++w)
-                            vm[r][w] = 2 * c + (r & 1) + 8 * (r >> 1) < seen ? v[r][w] : 0u;
-#pragma unroll
-                    for (int w = 0; w < D / 32; ++w) {
-                        uint32_t a[2][4];
-                        v_operands<D>(a, vm, w);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                float part[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma16816(part, a[k][0], a[k][1], a[k][2], a[k][3], pb[t][0], pb[t][1]);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    if ((row0 + 8 * t + 2 * c + (j & 1)) % p.N == tq) acc[t][2 * w + k][j] += part[j];
+                            for (int j = 0; j < D / 128; ++j) {
+                                const uint4 y = lds16(at_v + (r >> 1) * 1024 + j * (kTile * 128));
+                                v[r][4 * j] = y.x;
+                                v[r][4 * j + 1] = y.y;
+                                v[r][4 * j + 2] = y.z;
+                                v[r][4 * j + 3] = y.w;
                             }
+                        }
+                    }
+                    if (edge[u]) {  // what lies behind the sequence's end may be anything
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (tok0[u] + tau<D>(2 * c + (r & 1)) + 8 * (r >> 1) >= len)
+#pragma unroll
+                                for (int w = 0; w < D / 32; ++w) v[r][w] = 0u;
+                    }
+                    // A NaN code among tokens that some rows do not see must not reach
+                    // those rows (0 * NaN): then the product is taken for each query token by
+                    // itself, with only the values that it sees.
+                    bool special = false;
+                    if (edge[u] && p.causal && p.N > 1) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int w = 0; w < D / 32; ++w) special |= has_nan_code(v[r][w]);
+                        special = __any_sync(0xffffffffu, special);
+                    }
+                    if (special) {
+                        for (int tq = 0; tq < p.N; ++tq) {
+                            const int seen = len - p.N + tq + 1 - tok0[u];
+                            VWords<D> vm;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                                for (int w = 0; w < D / 32; ++w)
+                                    vm[r][w] = tau<D>(2 * c + (r & 1)) + 8 * (r >> 1) < seen ? v[r][w] : 0u;
+#pragma unroll
+                            for (int w = 0; w < D / 32; ++w) {
+                                uint32_t a[2][4];
+                                v_operands<D>(a, vm, w);
+#pragma unroll
+                                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) {
+                                        float part[4] = {0.f, 0.f, 0.f, 0.f};
+                                        mma16816(part, a[k][0], a[k][1], a[k][2], a[k][3], pb[u][t][0], pb[u][t][1]);
+#pragma unroll
+                                        for (int j = 0; j < 4; ++j)
+                                            if ((row0 + 8 * t + 2 * c + (j & 1)) % p.N == tq) acc[t][2 * w + k][j] += part[j];
+                                    }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < D / 32; ++w) {
+                            uint32_t a[2][4];
+                            v_operands<D>(a, v, w);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+                                    mma16816(acc[t][2 * w + k], a[k][0], a[k][1], a[k][2], a[k][3], pb[u][t][0], pb[u][t][1]);
+                        }
                     }
                 }
-            } else {
-#pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    uint32_t a[2][4];
-                    v_operands<D>(a, v, w);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            mma16816(acc[t][2 * w + k], a[k][0], a[k][1], a[k][2], a[k][3], pb[t][0], pb[t][1]);
-                }
+                __syncwarp();  // every lane has taken the values
+                if (i + u + S < n_pad) load(i + u + S, slot0 + u, false);
             }
+            slot0 += T;
+            if (slot0 == S) slot0 = 0, parity ^= 1;
         }
-        cp_wait<0>();
-        __syncwarp();  // every lane has read its last stage: the ring becomes the merge's rows
-
-        // ---- this warp's part, normalised
-        float *rows = reinterpret_cast<float *>(ring);
+        // ---- the next pair's copies start before this one's result is written
+        const long long row = q_row;
+        const bool whole = t0 == 0 && n_own == nb;
+        const long long part = ((((long long)chunk * p.workers + worker) * 2) + (t0 == 0 ? 1 : 0)) * 8 * NT;
+        n_own = 0;
+        more = !failed && next_pair();
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -512,122 +651,97 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                if (failed) sum = __int_as_float(0x7fffffff);
                 const float f = sum == 0.f ? 0.f : ex2_approx(n[t][k] - m[t][k] - 7.f) / sum;
                 const int r = 8 * t + 2 * c + k;
-                if (g == 0) s_ml[warp][r] = make_float2(m[t][k], sum);
+                if (row0 + r >= p.rows) continue;
+                if (g == 0) {
+                    if (whole)
+                        p.lse[row + r] = row_lse(m[t][k], sum);
+                    else
+                        p.ml_part[part + r] = make_float2(m[t][k], sum);
+                }
                 // components 4 w .. 4 w + 3 of the lane's run
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w) {
                     const int d0 = D == 64 ? 8 * g + 4 * w : 128 * (w >> 2) + 16 * g + 4 * (w & 3);
-                    *reinterpret_cast<float4 *>(rows + r * RS + d0) =
-                        make_float4(acc[t][2 * w][k] * f, acc[t][2 * w][k + 2] * f, acc[t][2 * w + 1][k] * f,
-                                    acc[t][2 * w + 1][k + 2] * f);
+                    const float4 o = make_float4(acc[t][2 * w][k] * f, acc[t][2 * w][k + 2] * f,
+                                                 acc[t][2 * w + 1][k] * f, acc[t][2 * w + 1][k + 2] * f);
+                    if (!whole)
+                        *reinterpret_cast<float4 *>(p.o_part + (part + r) * D + d0) = o;
+                    else if (p.o_bf16)
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + (row + r) * D + d0) =
+                            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+                    else
+                        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + (row + r) * D + d0) = o;
                 }
             }
-        __syncthreads();
-
-        // ---- merge the warps: 4 components of a row for each thread
-        const bool whole = t0 == 0 && t1 == nb;
-        const long long part = ((long long)chunk * p.workers + worker) * 2 + (t0 == 0 ? 1 : 0);
-        for (int k = threadIdx.x; k < 8 * NT * (D / 4); k += kThreads) {
-            const int r = k / (D / 4), d0 = 4 * (k % (D / 4));
-            if (row0 + r >= p.rows) break;
-            float2 ml[kWarps];
-            float top = neg_inf();
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                ml[w] = s_ml[w][r];
-                top = fmaxf(top, ml[w].x);
-            }
-            const float ref = top == neg_inf() ? 0.f : top;
-            float sum = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float a = ex2_approx(ml[w].x - ref) * ml[w].y;
-                const float4 y = *reinterpret_cast<const float4 *>(smem + w * kRingBytes<D> + 4 * (r * RS + d0));
-                sum += a;
-                o.x += a * y.x;
-                o.y += a * y.y;
-                o.z += a * y.z;
-                o.w += a * y.w;
-            }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-            if (!whole) {
-                *reinterpret_cast<float4 *>(p.o_part + (part * 8 * NT + r) * D + d0) = o;
-                if (d0 == 0) p.ml_part[part * 8 * NT + r] = make_float2(top, sum);
-            } else {
-                const long long at_o = (q_row + r) * D + d0;
-                if (p.o_bf16)
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at_o) =
-                        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-                else
-                    *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at_o) = o;
-                if (d0 == 0) p.lse[q_row + r] = sum == 0.f ? neg_inf() : (ref + log2f(sum)) * 0.693147180559945f;
-            }
-        }
-        __syncthreads();  // before the next segment's copies reach the rows
     }
 }
 
-constexpr int kMergeWarps = 8;
-
 // The rows whose keys several workers had, and those without keys.  WPR warps
-// for each row share its parts; lane i has components [i D / 32, (i + 1) D / 32).
-// Bound by latency: the plan is found again while the first kernel still runs.
+// for each row share its parts (part i is warp i % WPR's); lane i has components
+// [i D / 32, (i + 1) D / 32).  Bound by latency: the plan is found again while the
+// first kernel still runs, then a warp reads the statistics of 32 parts at a
+// time and their outputs, several in flight.
+template <int WPR> constexpr int kMergeWarps = WPR < 4 ? 4 : WPR;
+
 template <int D, int WPR>
-__global__ void __launch_bounds__(32 * kMergeWarps) fa_cache_merge_kernel(const __grid_constant__ Params p, int nt8) {
-    constexpr int W = D / 32;
-    __shared__ float s_o[WPR > 1 ? kMergeWarps : 1][D];
-    __shared__ float2 s_ml[kMergeWarps];
+__global__ void __launch_bounds__(32 * kMergeWarps<WPR>) fa_cache_merge_kernel(const __grid_constant__ Params p, int nt8) {
+    constexpr int W = D / 32, WARPS = kMergeWarps<WPR>;
+    __shared__ float s_o[WPR > 1 ? WARPS : 1][WPR > 1 ? D : 1];
+    __shared__ float2 s_ml[WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * (kMergeWarps / WPR) + warp / WPR;
+    const long long row = (long long)blockIdx.x * (WARPS / WPR) + warp / WPR;
     const int sub = warp % WPR;
-    const Plan plan = make_plan(p);
+    const Plan plan = make_plan<D>(p);
     const int unit = (int)(row / p.rows), r = (int)(row - (long long)unit * p.rows);
     const int b = unit / p.c.H_kv, h = unit - b * p.c.H_kv;
     const bool inside = b < p.c.B;
-    long long first = 0;
-    for (int i = lane; i < min(b, p.c.B); i += 32) first += seq_tiles(p, i);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) first += __shfl_xor_sync(0xffffffffu, first, i);
+    int first = 0;
+    for (int i = lane; i < min(b, p.c.B); i += 32) first += pair_cost(seq_tiles(p, i));
+    first = __reduce_add_sync(0xffffffffu, first);
     const int nb = inside ? seq_tiles(p, b) : 0;
-    const long long s = first * p.c.H_kv + (long long)h * nb;
-    const long long w0 = s / plan.per, w1 = nb ? (s + nb - 1) / plan.per : w0;
+    const int s = first * p.c.H_kv + h * pair_cost(nb) + kPairCost;  // its first tile's place
+    const int w0 = s / plan.per, w1 = nb ? (s + nb - 1) / plan.per : w0;
     // The results of the first kernel are complete from here on.  Every thread
     // waits, so that this grid does not end before the other.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!inside || (nb && w0 == w1)) return;  // the one worker that had it has written it
-    const int n = nb ? (int)(w1 - w0) + 1 : 0;
+    const int n = nb ? w1 - w0 + 1 : 0;
     const int chunk = r / nt8;
-    // part i is worker w0 + i's; the first begins the segment, the others continue it
+    // part i is worker w0 + i's; the first begins the pair, the others continue it
     const long long base = ((long long)chunk * p.workers + w0) * 2;
     const int rr = r - chunk * nt8;
     auto index = [&](int i) { return (base + 2 * i + (i == 0 ? 1 : 0)) * nt8 + rr; };
 
-    float top = neg_inf();
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, p.ml_part[index(i)].x);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    const float ref = top == neg_inf() ? 0.f : top;
     float o[W];
 #pragma unroll
     for (int k = 0; k < W; ++k) o[k] = 0.f;
-    float sum = 0.f;
-    constexpr int UN = 4;
-    for (int i0 = sub; i0 < n; i0 += UN * WPR) {
-        float a[UN], y[UN][W];
+    float top = neg_inf(), sum = 0.f;
+    for (int i0 = sub; i0 < n; i0 += 32 * WPR) {
+        const int own = i0 + lane * WPR;
+        float2 ml = make_float2(neg_inf(), 0.f);
+        if (own < n) ml = p.ml_part[index(own)];
+        float t = fmaxf(ml.x, top);
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int i = i0 + u * WPR;
-            a[u] = 0.f;
+        for (int i = 16; i > 0; i >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, i));
+        if (t != neg_inf()) {  // else nothing has been seen: there is nothing to rescale
+            const float f = ex2_approx(top - t);
+            sum *= f;
 #pragma unroll
-            for (int k = 0; k < W; ++k) y[u][k] = 0.f;
-            if (i < n) {
-                const float2 ml = p.ml_part[index(i)];
-                a[u] = ex2_approx(ml.x - ref) * ml.y;
-                const float *src = p.o_part + index(i) * D + lane * W;
+            for (int k = 0; k < W; ++k) o[k] *= f;
+        }
+        top = t;
+        const float a = ex2_approx(ml.x - (t == neg_inf() ? 0.f : t)) * ml.y;
+        sum += a;  // this lane's parts; the lanes are added at the end
+        const int m = min((n - i0 + WPR - 1) / WPR, 32);
+        constexpr int UN = W > 4 ? 4 : 8;
+        for (int j0 = 0; j0 < m; j0 += UN) {
+            float y[UN][W];
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const float *src = p.o_part + index(i0 + min(j0 + u, m - 1) * WPR) * D + lane * W;
                 if constexpr (W % 4 == 0) {
 #pragma unroll
                     for (int k = 0; k < W; k += 4) {
@@ -639,27 +753,37 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_cache_merge_kernel(const 
                     y[u][0] = z.x, y[u][1] = z.y;
                 }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            sum += a[u];
+            for (int u = 0; u < UN; ++u) {
+                if (j0 + u >= m) break;
+                const float w = __shfl_sync(0xffffffffu, a, j0 + u);
 #pragma unroll
-            for (int k = 0; k < W; ++k) o[k] += a[u] * y[u][k];
+                for (int k = 0; k < W; ++k) o[k] += w * y[u][k];
+            }
         }
     }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
     if constexpr (WPR > 1) {
 #pragma unroll
         for (int k = 0; k < W; ++k) s_o[warp][lane * W + k] = o[k];
-        if (lane == 0) s_ml[warp].y = sum;
+        if (lane == 0) s_ml[warp] = make_float2(top, sum);
         __syncthreads();
         if (warp) return;
-        sum = 0.f;
+        const float2 ml = lane < WPR ? s_ml[lane] : make_float2(neg_inf(), 0.f);
+        top = ml.x;
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+        const float f = ex2_approx(ml.x - (top == neg_inf() ? 0.f : top));
+        sum = f * ml.y;
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
 #pragma unroll
         for (int k = 0; k < W; ++k) o[k] = 0.f;
-        for (int w = 0; w < WPR; ++w) {
-            sum += s_ml[w].y;
+        for (int w = 0; w < min(WPR, n); ++w) {
+            const float fw = __shfl_sync(0xffffffffu, f, w);
 #pragma unroll
-            for (int k = 0; k < W; ++k) o[k] += s_o[w][lane * W + k];
+            for (int k = 0; k < W; ++k) o[k] += fw * s_o[w][lane * W + k];
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -671,7 +795,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_cache_merge_kernel(const 
         else
             *reinterpret_cast<float2 *>(static_cast<float *>(p.o) + dst + k) = make_float2(o[k] * inv, o[k + 1] * inv);
     }
-    if (lane == 0) p.lse[row] = sum == 0.f ? neg_inf() : (ref + log2f(sum)) * 0.693147180559945f;
+    if (lane == 0) p.lse[row] = row_lse(top, sum);
 }
 
 }  // namespace cattn

@@ -2,6 +2,8 @@
 // of the C ABI; hidden symbols).
 #pragma once
 
+#include <cuda.h>
+
 #include "fa.h"
 
 namespace fa_detail {
@@ -16,6 +18,10 @@ fa_status probe_current_device();
 
 // The same, with the device's ordinal and its number of SMs.
 fa_status current_device(int *dev, int *num_sms);
+
+// The tensor map of a cache's codes: [tiles][lines][line_bytes] with boxes of one tile's
+// lines by 128 bytes, 128-byte swizzle.
+fa_status encode_cache_map(CUtensorMap *map, const void *codes, long long tiles, int lines, int line_bytes);
 
 // Device ordinals are below this (current_device refuses others).
 constexpr int kMaxDevices = 64;

@@ -485,6 +485,11 @@ typedef struct {
                                   caller, nothing in it has to be set, and not shared by
                                   calls whose executions overlap                         */
     size_t workspace_bytes;
+    uint32_t timeout_ms;       /* per-wait time limit on the device; 0 = 2000 ms.  After
+                                  FA_ERR_DEVICE_TIMEOUT all of o and lse is undefined    */
+    int test_drop_load;        /* test only, 0 in every normal call; n > 0: the first CTA's
+                                  first warp never loads its n-th tile of keys and values,
+                                  so that the wait for it runs out                       */
 } fa_cache_attn_params;
 
 /* Scratch bytes fa_cache_attn needs for *p; host arithmetic only; 0 for a NULL p. */

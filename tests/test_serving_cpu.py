@@ -142,7 +142,7 @@ CACHE_REFUSALS = [
     (dict(table_stride=-8), fb.FA_ERR_INVALID_ARGUMENT), (dict(page=48), fb.FA_ERR_UNSUPPORTED),
     (dict(page=8), fb.FA_ERR_UNSUPPORTED), (dict(page=256), fb.FA_ERR_UNSUPPORTED), (dict(d=96), fb.FA_ERR_UNSUPPORTED),
     (dict(d=0), fb.FA_ERR_UNSUPPORTED), (dict(max_pages=1 << 30), fb.FA_ERR_INVALID_ARGUMENT),
-    (dict(B=1 << 20, H_kv=1 << 20), fb.FA_ERR_INVALID_ARGUMENT),
+    (dict(B=1 << 20, H_kv=1 << 20), fb.FA_ERR_INVALID_ARGUMENT), (dict(n_pages=1 << 30, H_kv=8), fb.FA_ERR_INVALID_ARGUMENT),
     (dict(k=None), fb.FA_ERR_INVALID_ARGUMENT), (dict(v=None), fb.FA_ERR_INVALID_ARGUMENT),
     (dict(k_scale=None), fb.FA_ERR_INVALID_ARGUMENT), (dict(v_scale=None), fb.FA_ERR_INVALID_ARGUMENT),
     (dict(table=None), fb.FA_ERR_INVALID_ARGUMENT), (dict(k=0x10008), fb.FA_ERR_MISALIGNED),
@@ -214,7 +214,8 @@ def test_gather_refusals(kw, expect):
     (dict(k_len=None), fb.FA_ERR_INVALID_ARGUMENT), (dict(workspace=None), fb.FA_ERR_INVALID_ARGUMENT),
     (dict(workspace_bytes=16), fb.FA_ERR_INVALID_ARGUMENT), (dict(q=0x60008), fb.FA_ERR_MISALIGNED),
     (dict(o=0x70004), fb.FA_ERR_MISALIGNED), (dict(lse=0x80002), fb.FA_ERR_MISALIGNED),
-    (dict(workspace=0xa0008), fb.FA_ERR_MISALIGNED), (dict(H=1 << 20, N=1 << 20), fb.FA_ERR_INVALID_ARGUMENT),
+    (dict(workspace=0xa0008), fb.FA_ERR_MISALIGNED), (dict(test_drop_load=-1), fb.FA_ERR_INVALID_ARGUMENT),
+    (dict(H=1 << 20, N=1 << 20), fb.FA_ERR_INVALID_ARGUMENT),
     (dict(H=0), fb.FA_OK), (dict(N=0), fb.FA_OK),
 ])
 def test_attn_refusals(kw, expect):
@@ -230,10 +231,10 @@ def test_null_params():
 
 def test_attn_workspace_bytes():
     size = lambda cache=None, **kw: fb.load().fa_cache_attn_workspace_bytes(ctypes.byref(_attn_params(cache, **kw)))  # noqa: E731
-    # one pair of slots of 8 rows for each worker, 640 workers at most
-    assert 0 < size() <= 640 * 2 * 8 * (128 + 2) * 4
-    assert size(dict(B=1, H_kv=1, max_pages=1), H=1) == 1 * 2 * 8 * (128 + 2) * 4   # 4 tiles: one worker
-    assert size(dict(B=64, max_pages=128)) == 640 * 2 * 8 * (128 + 2) * 4
+    # one pair of slots of 8 rows for each worker, 2560 workers at most
+    assert 0 < size() <= 2560 * 2 * 8 * (128 + 2) * 4
+    assert size(dict(B=1, H_kv=1, max_pages=1), H=1) == 4 * 2 * 8 * (128 + 2) * 4   # 4 tiles: no more workers
+    assert size(dict(B=64, max_pages=128)) == 2560 * 2 * 8 * (128 + 2) * 4
     assert size(H=64) >= size(H=8)
     assert size(H=0) == size(N=0) == size(H=3) == size(dict(page=5)) == size(dict(B=0)) == 0
     assert fb.status_string(fb.FA_ERR_BAD_PAGE) == "FA_ERR_BAD_PAGE"

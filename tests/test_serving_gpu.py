@@ -531,6 +531,25 @@ def test_attention_bad_pages_are_left_out():
     assert (o[1] == 0).all() and torch.isneginf(lse[1]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("drop", [1, 5])
+def test_attention_wait_that_runs_out(d, drop):
+    """A tile that is never loaded ends the wait for it, with the status and without a hang; the next
+    call is sound."""
+    lens = [2000]
+    pool = ref.pool(46, lens, 1, 16, d)
+    c = cache_of(pool)
+    q = torch.randn(1, 4, 1, d, generator=torch.Generator().manual_seed(15)).to(BF16)
+    status = ints([0])
+    # 125 tiles: drop = 5 is past what one of few workers has, so the table is made long for one head
+    long = fa.PagedCache(c.k, c.v, c.k_scale, c.v_scale, c.table.repeat(1, 200).contiguous())
+    n = ints([2000 * 200])
+    fa.cache_attention(long, q.to(dev()), n, True, 0.1, dev_status=status, timeout_ms=20, test_drop_load=drop)
+    assert fa.read_device_status(status) == fb.FA_ERR_DEVICE_TIMEOUT
+    o, lse = run_attention(q, pool, lens, True, 0.1, cache=c)
+    check_attention(o, lse, q, pool, lens, True, 0.1, 16)
+
+
 def test_attention_shared_pages_length_past_the_table_and_strided_table():
     page, d = 32, 128
     pool = ref.pool(39, [200], 2, page, d)
