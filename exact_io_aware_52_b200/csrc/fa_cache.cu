@@ -194,11 +194,20 @@ fa_status fa_cache_append(const fa_cache_append_params *p, void *stream) {
         std::memcpy(kp.step, p->rotary->step, sizeof(uint64_t) * (kp.dim / 2));
         vec = vec && kp.dim % 16 == 0;
     }
-    const long long blocks = 2LL * c.B * c.H_kv * kp.pages;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (vec && (long long)p->N * (c.d / 16) <= 32) {
+        const long long blocks = ((long long)c.B * c.H_kv + fa::kFewWarps - 1) / fa::kFewWarps;
+        fa::fa_cache_append_few_kernel<<<(unsigned)blocks, 32 * fa::kFewWarps, 0, s>>>(kp);
+        return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    }
+    // as many heads in a block, which share the sines, as leave every SM four blocks
+    const long long touched = (long long)c.B * kp.pages;
+    kp.group = c.H_kv;
+    while (kp.group > 1 && touched * ((c.H_kv + kp.group - 1) / kp.group) < 4LL * sms) kp.group = (kp.group + 1) / 2;
+    const long long blocks = touched * ((c.H_kv + kp.group - 1) / kp.group);
     if (blocks > kMaxInt) return FA_ERR_INVALID_ARGUMENT;
     const int slots = c.page * (c.d / 16);  // 64 .. 2048 of 16 components
     const int threads = slots < 512 ? slots : 512;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (slots / threads) {
         case 1: launch_append<1>(kp, vec, (unsigned)blocks, threads, s); break;
         case 2: launch_append<2>(kp, vec, (unsigned)blocks, threads, s); break;
@@ -226,7 +235,7 @@ fa_status fa_cache_gather(const fa_cache_gather_params *p, void *stream) {
     kp.v = static_cast<uint16_t *>(p->v);
     kp.N_k = p->N_k;
     kp.status = p->dev_status;
-    const int per_block = fa::kGatherThreads * fa::kGatherItems / (c.d / 16);
+    const int per_block = fa::kGatherThreads * fa::kGatherItems / (c.d / 8);
     kp.row_blocks = (int)(((long long)p->N_k + per_block - 1) / per_block);
     const long long blocks = (long long)c.B * c.H_kv * kp.row_blocks;
     if (blocks > kMaxInt) return FA_ERR_INVALID_ARGUMENT;

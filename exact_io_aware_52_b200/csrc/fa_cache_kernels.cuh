@@ -36,6 +36,7 @@ struct AppendParams {
     long long xs[2][3];
     int N;
     int pages;                  // pages that N tokens can touch, at most
+    int group;                  // heads that one block handles
     const int32_t *start, *n_new;
     int32_t *status;
     int dim, interleaved;       // dim 0: keys are not turned
@@ -56,12 +57,15 @@ __device__ __forceinline__ float page_scale(float amax) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Four values times inv as E4M3 codes; infinities and NaN give the code NaN
-// (v * 0 is NaN for them and 0 for the others; the conversion would saturate
-// an infinity).
+// Four values times inv as E4M3 codes.  NaN gives the code NaN; SPECIAL: infinities
+// do so too (v * 0 is NaN for them and 0 for the others; the conversion would saturate them).
+template <bool SPECIAL>
 __device__ __forceinline__ uint32_t codes4(const float *v, float inv) {
-    return pack_e4m3x4(fmaf(v[0], inv, v[0] * 0.f), fmaf(v[1], inv, v[1] * 0.f), fmaf(v[2], inv, v[2] * 0.f),
-                       fmaf(v[3], inv, v[3] * 0.f));
+    if constexpr (SPECIAL)
+        return pack_e4m3x4(fmaf(v[0], inv, v[0] * 0.f), fmaf(v[1], inv, v[1] * 0.f), fmaf(v[2], inv, v[2] * 0.f),
+                           fmaf(v[3], inv, v[3] * 0.f));
+    else
+        return pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
 }
 
 // The four values of a word of E4M3 codes.
@@ -97,112 +101,280 @@ __device__ __forceinline__ float turned_component(const AppendParams &p, const u
     return first ? a : b;
 }
 
-// One block per (sequence, touched page, head, K or V).  Bound by memory: 2
-// bytes read and 1 written per component.  The page's new values stay in
-// registers between the maximum and the rounding (SPT slots of 16 components
-// a thread), so they are read once; the block owns the page, so the scale needs
-// no atomics and the result no order.
-template <int SPT, bool VEC>
-__global__ void __launch_bounds__(512) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
-    __shared__ uint64_t step[FA_ROTARY_MAX_DIM / 2];
-    __shared__ uint32_t s_max[16];
+// Where a block's (or warp's) new tokens lie: slots [s0, s1) of one page, the first of them
+// the sequence's new token t0.
+struct Touched {
+    int page_id, s0, s1, t0;
+    long long lo;  // position of the page's slot 0
+};
+// The pt-th page that sequence b's new tokens touch; false if there is none, or if it
+// is bad, which is reported.  The same for all threads of a block.
+__device__ __forceinline__ bool touched_page(const AppendParams &p, int b, int pt, bool reporter, Touched &r) {
     const CacheView &c = p.c;
-    const int kv = blockIdx.x & 1;
-    int u = blockIdx.x >> 1;
-    const int h = u % c.H_kv;
-    u /= c.H_kv;
-    const int pt = u % p.pages, b = u / p.pages;
-
     const int start = p.start[b];
     int n = p.n_new ? p.n_new[b] : p.N;
     n = n < 0 ? 0 : (n > p.N ? p.N : n);
-    if (n == 0) return;
+    if (n == 0) return false;
     if (start < 0) {
-        if (threadIdx.x == 0) report_bad_page(p.status);
-        return;
+        if (reporter) report_bad_page(p.status);
+        return false;
     }
-    const long long first = start, end = first + n;                 // positions
+    const long long first = start, end = first + n;
     const long long page_i = (first >> c.page_log2) + pt;
-    const long long lo = page_i << c.page_log2;                     // the page's first position
-    if (lo >= end) return;
-    const int page_id = page_i < c.max_pages ? c.table[b * c.table_stride + page_i] : -1;
-    if (page_id < 0 || page_id >= c.n_pages) {
-        if (threadIdx.x == 0) report_bad_page(p.status);
-        return;
+    r.lo = page_i << c.page_log2;
+    if (r.lo >= end) return false;
+    r.page_id = page_i < c.max_pages ? c.table[b * c.table_stride + page_i] : -1;
+    if (r.page_id < 0 || r.page_id >= c.n_pages) {
+        if (reporter) report_bad_page(p.status);
+        return false;
     }
-    const int s0 = first > lo ? (int)(first - lo) : 0;              // new tokens are in slots [s0, s1)
-    const int s1 = end - lo < c.page ? (int)(end - lo) : c.page;
-    const int dim = kv ? 0 : p.dim;
+    r.s0 = first > r.lo ? (int)(first - r.lo) : 0;
+    r.s1 = end - r.lo < c.page ? (int)(end - r.lo) : c.page;
+    r.t0 = (int)(r.lo + r.s0 - first);
+    return true;
+}
+
+// A slot of 16 components of a new key (turned by cs, sn) or value in fp32; `at` says where its two
+// runs lie.
+template <bool VEC>
+__device__ __forceinline__ void load_slot(const AppendParams &p, const uint64_t *step, const uint16_t *row, int slot,
+                                          const RotarySlot &at, int dim, int pos, const float (&cs)[8],
+                                          const float (&sn)[8], float (&v)[16]) {
+    if constexpr (VEC) {
+        load8(row + at.a, v);
+        load8(row + at.b, v + 8);
+        if (at.rotated) rotary_turn_slot(v, cs, sn, p.interleaved);
+    } else {
+        for (int j = 0; j < 16; ++j)
+            v[j] = dim ? turned_component(p, step, row, 16 * slot + j, pos) : load1(row + 16 * slot + j);
+    }
+}
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Largest magnitude as bits, which order as the magnitudes do; from kInfBits on it is not finite.
+__device__ __forceinline__ uint32_t slot_amax(const float (&v)[16]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    return m;
+}
+// Of the finite ones.
+__device__ __forceinline__ uint32_t slot_amax_finite(const float (&v)[16]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t u = __float_as_uint(v[j]) & 0x7fffffffu;
+        if (u < kInfBits) m = max(m, u);
+    }
+    return m;
+}
+
+__device__ __forceinline__ void store_slot(uint8_t *row, const RotarySlot &at, const float (&v)[16], float inv,
+                                           bool special) {
+    uint2 a, b;
+    if (special) {
+        a = make_uint2(codes4<true>(v, inv), codes4<true>(v + 4, inv));
+        b = make_uint2(codes4<true>(v + 8, inv), codes4<true>(v + 12, inv));
+    } else {
+        a = make_uint2(codes4<false>(v, inv), codes4<false>(v + 4, inv));
+        b = make_uint2(codes4<false>(v + 8, inv), codes4<false>(v + 12, inv));
+    }
+    if (at.b == at.a + 8) {
+        *reinterpret_cast<uint4 *>(row + at.a) = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+        *reinterpret_cast<uint2 *>(row + at.a) = a;
+        *reinterpret_cast<uint2 *>(row + at.b) = b;
+    }
+}
+
+// 16 codes of a page that grows.
+__device__ __forceinline__ void rescale_run(uint8_t *run, float ratio) {
+    uint4 w = *reinterpret_cast<const uint4 *>(run);
+    uint32_t *q = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float o[4];
+        values4(q[j], o);
+        q[j] = codes4<true>(o, ratio);
+    }
+    *reinterpret_cast<uint4 *>(run) = w;
+}
+
+// One block per (sequence, touched page, group of heads): it owns the page's codes and scales of
+// its heads, so that nothing needs atomics and no order of blocks changes the result.  A
+// thread has the same SPT slots (16 components of a token) of every head, so that the
+// sines and cosines, several times the work of the rest, are computed once for a group.
+// A head's keys and values are read once and stay in registers between the maximum
+// and the rounding.  Bound by memory: 2 bytes read and 1 written per component.
+template <int SPT, bool VEC>
+__global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
+    __shared__ uint64_t step[FA_ROTARY_MAX_DIM / 2];
+    __shared__ uint2 s_max[2][16];
+    const CacheView &c = p.c;
+    const int groups = (c.H_kv + p.group - 1) / p.group;
+    const int h0 = (blockIdx.x % groups) * p.group, h1 = min(h0 + p.group, c.H_kv);
+    const int u = blockIdx.x / groups;
+    const int pt = u % p.pages, b = u / p.pages;
+    Touched pg;
+    if (!touched_page(p, b, pt, threadIdx.x == 0, pg)) return;
+    const int dim = p.dim;
     if (dim) {
         for (int i = threadIdx.x; i < (dim >> 1); i += blockDim.x) step[i] = p.step[i];
         __syncthreads();
     }
+    const int per_row = c.d >> 4, row_log2 = 31 - __clz(per_row);
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    float cs[SPT][8], sn[SPT][8];
+    RotarySlot at[SPT];
+#pragma unroll
+    for (int i = 0; i < SPT; ++i) {
+        const int k = threadIdx.x + i * blockDim.x;
+        const int t = k >> row_log2, slot = k & (per_row - 1);
+        at[i] = rotary_slot(slot, VEC ? dim : 0, p.interleaved);
+        if (VEC && at[i].rotated && t >= pg.s0 && t < pg.s1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                rotary_cs(step[8 * slot + j], (int)(pg.lo + t), p.amplitude, 1.f, cs[i][j], sn[i][j]);
+        }
+    }
+    const uint16_t *xk = p.x[0] + b * p.xs[0][0] + (pg.t0 - pg.s0) * p.xs[0][2];
+    const uint16_t *xv = p.x[1] + b * p.xs[1][0] + (pg.t0 - pg.s0) * p.xs[1][2];
 
-    const int per_row = c.d >> 4;                                   // slots of 16 components in a token
-    const uint16_t *x = p.x[kv] + b * p.xs[kv][0] + h * p.xs[kv][1];
-    float v[SPT][16];
-    uint32_t amax = 0;
+    for (int h = h0; h < h1; ++h) {
+        float k[SPT][16], v[SPT][16];
+        uint32_t mk = 0, mv = 0;
 #pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-        const int k = threadIdx.x + i * blockDim.x;
-        const int t = k / per_row, slot = k - t * per_row;
-        if (t < s0 || t >= s1) continue;
-        const int pos = (int)(lo + t);
-        const uint16_t *row = x + (lo + t - first) * p.xs[kv][2];
-        if constexpr (VEC) {
-            const RotarySlot at = rotary_slot(slot, dim, p.interleaved);
-            load8(row + at.a, v[i]);
-            load8(row + at.b, v[i] + 8);
-            if (at.rotated) {
-                float cs[8], sn[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) rotary_cs(step[8 * slot + j], pos, p.amplitude, 1.f, cs[j], sn[j]);
-                rotary_turn_slot(v[i], cs, sn, p.interleaved);
-            }
-        } else {
-            for (int j = 0; j < 16; ++j)
-                v[i][j] = dim ? turned_component(p, step, row, 16 * slot + j, pos) : load1(row + 16 * slot + j);
+        for (int i = 0; i < SPT; ++i) {
+            const int kk = threadIdx.x + i * blockDim.x;
+            const int t = kk >> row_log2, slot = kk & (per_row - 1);
+            if (t < pg.s0 || t >= pg.s1) continue;
+            const RotarySlot plain = rotary_slot(slot, 0, false);
+            load_slot<VEC>(p, step, xv + h * p.xs[1][1] + t * p.xs[1][2], slot, plain, 0, 0, cs[i], sn[i], v[i]);
+            load_slot<VEC>(p, step, xk + h * p.xs[0][1] + t * p.xs[0][2], slot, at[i], dim, (int)(pg.lo + t), cs[i], sn[i],
+                           k[i]);
+            mk = max(mk, slot_amax(k[i]));
+            mv = max(mv, slot_amax(v[i]));
         }
+        uint2 *sm = s_max[h & 1];  // the other one may still be read for the head before
+        auto block_max = [&]() {
+            mk = __reduce_max_sync(0xffffffffu, mk);
+            mv = __reduce_max_sync(0xffffffffu, mv);
+            if ((threadIdx.x & 31) == 0) sm[warp] = make_uint2(mk, mv);
+            __syncthreads();
+            for (int i = 0; i < warps; ++i) {
+                const uint2 x = sm[i];
+                mk = max(mk, x.x);
+                mv = max(mv, x.y);
+            }
+        };
+        const long long unit = (long long)pg.page_id * c.H_kv + h;
+        // read by all before thread 0 writes them
+        const float before_k = pg.s0 > 0 ? c.k_scale[unit] : 0.f, before_v = pg.s0 > 0 ? c.v_scale[unit] : 0.f;
+        block_max();
+        const bool special_k = mk >= kInfBits, special_v = mv >= kInfBits;
+        if (special_k || special_v) {  // rare; the same for the whole block
+            mk = mv = 0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const uint32_t m = __float_as_uint(v[i][j]) & 0x7fffffffu;
-            if (m < 0x7f800000u) amax = max(amax, m);               // finite magnitudes order as their bits
+            for (int i = 0; i < SPT; ++i) {
+                const int t = (threadIdx.x + i * blockDim.x) >> row_log2;
+                if (t < pg.s0 || t >= pg.s1) continue;
+                mk = max(mk, slot_amax_finite(k[i]));
+                mv = max(mv, slot_amax_finite(v[i]));
+            }
+            __syncthreads();
+            block_max();
+        }
+        const float now_k = fmaxf(before_k, page_scale(__uint_as_float(mk)));
+        const float now_v = fmaxf(before_v, page_scale(__uint_as_float(mv)));
+        const float inv_k = 1.f / now_k, inv_v = 1.f / now_v;
+        const bool grows_k = pg.s0 > 0 && now_k != before_k, grows_v = pg.s0 > 0 && now_v != before_v;
+        uint8_t *ck = c.k + unit * c.page * c.d, *cvv = c.v + unit * c.page * c.d;
+#pragma unroll
+        for (int i = 0; i < SPT; ++i) {
+            const int kk = threadIdx.x + i * blockDim.x;
+            const int t = kk >> row_log2, slot = kk & (per_row - 1);
+            if (t >= pg.s1) continue;
+            if (t >= pg.s0) {
+                store_slot(ck + t * c.d, at[i], k[i], inv_k, special_k);
+                store_slot(cvv + t * c.d, rotary_slot(slot, 0, false), v[i], inv_v, special_v);
+            } else {  // exact ratios for powers of two
+                if (grows_k) rescale_run(ck + t * c.d + 16 * slot, before_k * inv_k);
+                if (grows_v) rescale_run(cvv + t * c.d + 16 * slot, before_v * inv_v);
+            }
+        }
+        if (threadIdx.x == 0) {
+            if (pg.s0 == 0 || grows_k) c.k_scale[unit] = now_k;
+            if (pg.s0 == 0 || grows_v) c.v_scale[unit] = now_v;
         }
     }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
-    float *scale = (kv ? c.v_scale : c.k_scale) + (long long)page_id * c.H_kv + h;
-    const float before = s0 > 0 ? *scale : 0.f;                     // read by all before thread 0 writes it
-    __syncthreads();
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) amax = max(amax, s_max[i]);
-    const float now = fmaxf(before, page_scale(__uint_as_float(amax)));
-    const float inv = 1.f / now;
-    uint8_t *codes = (kv ? c.v : c.k) + ((long long)page_id * c.H_kv + h) * c.page * c.d;
-    const bool grows = s0 > 0 && now != before;
-    const float ratio = before * inv;                               // exact for powers of two
+}
+
+// The same for so few tokens that a warp holds them (N * d / 16 <= 32): one warp per
+// (sequence, head), lane (token, slot).  Bound by latency, and then a block of hundreds of
+// threads for a page of which one slot is new costs more than its work.
+constexpr int kFewWarps = 4;
+__global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(const __grid_constant__ AppendParams p) {
+    const CacheView &c = p.c;
+    const int lane = threadIdx.x & 31;
+    const long long unit_i = (long long)blockIdx.x * kFewWarps + (threadIdx.x >> 5);
+    const int b = (int)(unit_i / c.H_kv), h = (int)(unit_i - (long long)b * c.H_kv);
+    if (b >= c.B) return;
+    const int per_row = c.d >> 4, row_log2 = 31 - __clz(per_row);
+    const int i = lane >> row_log2, slot = lane & (per_row - 1);  // new token i
+    const RotarySlot at = rotary_slot(slot, p.dim, p.interleaved), plain = rotary_slot(slot, 0, false);
+    float k[16], v[16];
 #pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-        const int k = threadIdx.x + i * blockDim.x;
-        const int t = k / per_row, slot = k - t * per_row;
-        if (t >= s1) continue;
-        uint8_t *row = codes + t * c.d;
-        if (t >= s0) {
-            const RotarySlot at = rotary_slot(slot, VEC ? dim : 0, p.interleaved);
-            *reinterpret_cast<uint2 *>(row + at.a) = make_uint2(codes4(v[i], inv), codes4(v[i] + 4, inv));
-            *reinterpret_cast<uint2 *>(row + at.b) = make_uint2(codes4(v[i] + 8, inv), codes4(v[i] + 12, inv));
-        } else if (grows) {
-            uint4 w = *reinterpret_cast<const uint4 *>(row + 16 * slot);
-            uint32_t *q = reinterpret_cast<uint32_t *>(&w);
+    for (int j = 0; j < 16; ++j) k[j] = v[j] = 0.f;
+    const int start = p.start[b];
+    const int n = max(0, min(p.n_new ? p.n_new[b] : p.N, p.N));
+    if (i < n) {
+        const uint16_t *xk = p.x[0] + b * p.xs[0][0] + h * p.xs[0][1] + i * p.xs[0][2];
+        const uint16_t *xv = p.x[1] + b * p.xs[1][0] + h * p.xs[1][1] + i * p.xs[1][2];
+        load8(xk + at.a, k);
+        load8(xk + at.b, k + 8);
+        load8(xv + plain.a, v);
+        load8(xv + plain.b, v + 8);
+        if (at.rotated) {
+            float cs[8], sn[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float o[4];
-                values4(q[j], o);
-                q[j] = codes4(o, ratio);
-            }
-            *reinterpret_cast<uint4 *>(row + 16 * slot) = w;
+            for (int j = 0; j < 8; ++j) rotary_cs(p.step[8 * slot + j], start + i, p.amplitude, 1.f, cs[j], sn[j]);
+            rotary_turn_slot(k, cs, sn, p.interleaved);
         }
     }
-    if (threadIdx.x == 0) *scale = now;
+    const bool first_of_seq = h == 0 && lane == 0;
+    for (int pt = 0; pt < p.pages; ++pt) {
+        Touched pg;
+        if (!touched_page(p, b, pt, first_of_seq, pg)) continue;
+        const int t = i < n ? (int)((long long)start + i - pg.lo) : -1;  // this lane's slot in the page
+        const bool here = t >= pg.s0 && t < pg.s1;
+        const long long unit = (long long)pg.page_id * c.H_kv + h;
+        const float before_k = pg.s0 > 0 ? c.k_scale[unit] : 0.f, before_v = pg.s0 > 0 ? c.v_scale[unit] : 0.f;
+        uint32_t mk = __reduce_max_sync(0xffffffffu, here ? slot_amax(k) : 0u);
+        uint32_t mv = __reduce_max_sync(0xffffffffu, here ? slot_amax(v) : 0u);
+        const bool special_k = mk >= kInfBits, special_v = mv >= kInfBits;
+        if (special_k || special_v) {
+            mk = __reduce_max_sync(0xffffffffu, here ? slot_amax_finite(k) : 0u);
+            mv = __reduce_max_sync(0xffffffffu, here ? slot_amax_finite(v) : 0u);
+        }
+        const float now_k = fmaxf(before_k, page_scale(__uint_as_float(mk)));
+        const float now_v = fmaxf(before_v, page_scale(__uint_as_float(mv)));
+        const float inv_k = 1.f / now_k, inv_v = 1.f / now_v;
+        uint8_t *ck = c.k + unit * c.page * c.d, *cvv = c.v + unit * c.page * c.d;
+        if (here) {
+            store_slot(ck + t * c.d, at, k, inv_k, special_k);
+            store_slot(cvv + t * c.d, plain, v, inv_v, special_v);
+        }
+        const bool grows_k = pg.s0 > 0 && now_k != before_k, grows_v = pg.s0 > 0 && now_v != before_v;
+        if (grows_k)
+            for (int r = lane; r < pg.s0 * per_row; r += 32) rescale_run(ck + 16 * r, before_k * inv_k);
+        if (grows_v)
+            for (int r = lane; r < pg.s0 * per_row; r += 32) rescale_run(cvv + 16 * r, before_v * inv_v);
+        if (lane == 0) {
+            if (pg.s0 == 0 || grows_k) c.k_scale[unit] = now_k;
+            if (pg.s0 == 0 || grows_v) c.v_scale[unit] = now_v;
+        }
+    }
 }
 
 // ---------------------------------------------------------------- gather
@@ -216,64 +388,59 @@ struct GatherParams {
 };
 
 constexpr int kGatherThreads = 256;
-constexpr int kGatherItems = 4;  // 16-byte runs of codes a thread has in flight, of K and of V
+constexpr int kGatherItems = 4;  // runs of 8 codes a thread has in flight, of K and of V
 
-// 16 codes times scale as bf16.
-__device__ __forceinline__ void gather_store(uint16_t *dst, uint4 w, float scale) {
-    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-    uint32_t r[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float v[4];
-        values4(q[j], v);
-        r[2 * j] = pack_bf16x2(v[0] * scale, v[1] * scale);
-        r[2 * j + 1] = pack_bf16x2(v[2] * scale, v[3] * scale);
-    }
-    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+// 8 codes times scale as bf16.
+__device__ __forceinline__ void gather_store(uint16_t *dst, uint2 w, float scale) {
+    float v[8];
+    values4(w.x, v);
+    values4(w.y, v + 4);
+    *reinterpret_cast<uint4 *>(dst) =
+        make_uint4(pack_bf16x2(v[0] * scale, v[1] * scale), pack_bf16x2(v[2] * scale, v[3] * scale),
+                   pack_bf16x2(v[4] * scale, v[5] * scale), pack_bf16x2(v[6] * scale, v[7] * scale));
 }
 
 // Bound by memory: 1 byte read and 2 written per component.  One thread takes
-// runs of 16 components of one (sequence, head), of the keys and the values at
-// the same place (they share the page lookup); all its loads are issued before
-// its stores.
+// runs of 8 components of one (sequence, head), of the keys and the values at
+// the same place (they share the page lookup), so that a warp's stores are 512 bytes in
+// one piece; all its loads are issued before its stores.
 __global__ void __launch_bounds__(kGatherThreads) fa_cache_gather_kernel(const __grid_constant__ GatherParams p) {
     const CacheView &c = p.c;
     const int bh = blockIdx.x / p.row_blocks, part = blockIdx.x - bh * p.row_blocks;
     const int b = bh / c.H_kv, h = bh - b * c.H_kv;
-    const int runs = c.d >> 4;
+    const int runs = c.d >> 3, runs_log2 = 31 - __clz(runs);
     const long long cap = (long long)c.max_pages << c.page_log2;
-    const long long len = min((long long)max(p.k_len[b], 0), cap);
-    const int per_block = kGatherThreads * kGatherItems / runs;     // rows
-    uint4 kw[kGatherItems], vw[kGatherItems];
+    const int len = (int)min((long long)max(p.k_len[b], 0), cap);
+    const int row0 = part * (kGatherThreads * kGatherItems / runs);  // below N_k
+    const int32_t *table = c.table + b * c.table_stride;
+    uint2 kw[kGatherItems], vw[kGatherItems];
     float ks[kGatherItems], vs[kGatherItems];
 #pragma unroll
     for (int i = 0; i < kGatherItems; ++i) {
         const int k = threadIdx.x + i * kGatherThreads;
-        const int r = k / runs, run = k - r * runs;
-        const long long n = (long long)part * per_block + r;
-        kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
+        const long long n = (long long)row0 + (k >> runs_log2);
+        const int run = k & (runs - 1);
+        kw[i] = vw[i] = make_uint2(0, 0);
         ks[i] = vs[i] = 0.f;
         if (n >= p.N_k || n >= len) continue;
-        const int page_id = c.table[b * c.table_stride + (n >> c.page_log2)];
+        const int page_id = table[n >> c.page_log2];
         if (page_id < 0 || page_id >= c.n_pages) {
             if (run == 0) report_bad_page(p.status);
             continue;
         }
         const long long unit = (long long)page_id * c.H_kv + h;
-        const long long off = (unit * c.page + (n & (c.page - 1))) * c.d + 16 * run;
-        kw[i] = *reinterpret_cast<const uint4 *>(c.k + off);
-        vw[i] = *reinterpret_cast<const uint4 *>(c.v + off);
+        const long long off = (unit * c.page + (n & (c.page - 1))) * c.d + 8 * run;
+        kw[i] = __ldcs(reinterpret_cast<const uint2 *>(c.k + off));
+        vw[i] = __ldcs(reinterpret_cast<const uint2 *>(c.v + off));
         ks[i] = c.k_scale[unit];
         vs[i] = c.v_scale[unit];
     }
 #pragma unroll
     for (int i = 0; i < kGatherItems; ++i) {
         const int k = threadIdx.x + i * kGatherThreads;
-        const int r = k / runs, run = k - r * runs;
-        const long long n = (long long)part * per_block + r;
+        const long long n = (long long)row0 + (k >> runs_log2);
         if (n >= p.N_k) continue;
-        const long long off = ((long long)bh * p.N_k + n) * c.d + 16 * run;
+        const long long off = ((long long)bh * p.N_k + n) * c.d + 8 * (k & (runs - 1));
         gather_store(p.k + off, kw[i], ks[i]);
         gather_store(p.v + off, vw[i], vs[i]);
     }

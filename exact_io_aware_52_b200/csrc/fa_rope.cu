@@ -46,6 +46,35 @@ __device__ __forceinline__ T *rope_dst(const RopeParams &p, int h, int b, int n)
     return static_cast<T *>(t.y) + b * t.ys[0] + (h >= p.heads0 ? h - p.heads0 : h) * t.ys[1] + n * t.ys[2];
 }
 
+// A slot's 16 components as they are read: kept so while their loads are in flight, which takes half
+// the registers of fp32 for bf16.
+template <typename T> struct RawSlot;
+template <> struct RawSlot<uint16_t> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const uint16_t *x, const RotarySlot &at) {
+        a = __ldcs(reinterpret_cast<const uint4 *>(x + at.a));
+        b = __ldcs(reinterpret_cast<const uint4 *>(x + at.b));
+    }
+    __device__ __forceinline__ void get(float (&v)[16]) const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[2 * i] = bf16x2_lo(w[i]), v[2 * i + 1] = bf16x2_hi(w[i]);
+    }
+};
+template <> struct RawSlot<float> {
+    float4 a[4];
+    __device__ __forceinline__ void load(const float *x, const RotarySlot &at) {
+        a[0] = __ldcs(reinterpret_cast<const float4 *>(x + at.a));
+        a[1] = __ldcs(reinterpret_cast<const float4 *>(x + at.a) + 1);
+        a[2] = __ldcs(reinterpret_cast<const float4 *>(x + at.b));
+        a[3] = __ldcs(reinterpret_cast<const float4 *>(x + at.b) + 1);
+    }
+    __device__ __forceinline__ void get(float (&v)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * i] = a[i].x, v[4 * i + 1] = a[i].y, v[4 * i + 2] = a[i].z, v[4 * i + 3] = a[i].w;
+    }
+};
+
 // Bound by memory: every component is read once and written once.  One thread
 // has one slot (16 components) of one token and walks over `chunk` heads, so
 // that the 8 sines and cosines, which the heads share, are computed once for
@@ -53,7 +82,8 @@ __device__ __forceinline__ T *rope_dst(const RopeParams &p, int h, int b, int n)
 // loads in flight.  The lanes of a warp lie along the components and then
 // along the tokens: whole 128-byte lines whichever way the strides run.
 template <typename TI, typename TO>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 4 : 3)
+fa_rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ uint64_t step[FA_ROTARY_MAX_DIM / 2];
     if (threadIdx.x < (p.dim >> 1)) step[threadIdx.x] = p.step[threadIdx.x];
     __syncthreads();
@@ -70,26 +100,33 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < 8; ++j) rotary_cs(step[8 * slot + j], pos, p.amplitude, p.sign, c[j], s[j]);
     }
-    constexpr int UN = sizeof(TI) == 2 ? 4 : 2;
-    const int h0 = blockIdx.y * p.chunk;
-    const int h1 = min(h0 + p.chunk, p.heads);
-    for (int h = h0; h < h1; h += UN) {
-        float v[UN][16];
+    constexpr int UN = 2;
+    const int h0 = blockIdx.y * p.chunk, h1 = min(h0 + p.chunk, p.heads);
 #pragma unroll
-        for (int u = 0; u < UN; ++u)
-            if (h + u < h1) {
-                const TI *x = rope_src<TI>(p, h + u, b, n);
-                load8(x + at.a, v[u]);
-                load8(x + at.b, v[u] + 8);
-            }
+    for (int i = 0; i < 2; ++i) {
+        const RopeTensor &t = p.t[i];
+        const int off = i ? p.heads0 : 0;  // head h of the call is head h - off of the tensor
+        const int lo = max(h0, off) - off, hi = (i ? h1 : min(h1, p.heads0)) - off;
+        if (lo >= hi) continue;
+        const TI *x = static_cast<const TI *>(t.x) + b * t.xs[0] + lo * t.xs[1] + n * t.xs[2];
+        TO *y = static_cast<TO *>(t.y) + b * t.ys[0] + lo * t.ys[1] + n * t.ys[2];
+        for (int h = lo; h < hi; h += UN) {
+            RawSlot<TI> raw[UN];
 #pragma unroll
-        for (int u = 0; u < UN; ++u)
-            if (h + u < h1) {
-                if (at.rotated) rotary_turn_slot(v[u], c, s, p.interleaved);
-                TO *y = rope_dst<TO>(p, h + u, b, n);
-                store8(y + at.a, v[u]);
-                store8(y + at.b, v[u] + 8);
-            }
+            for (int u = 0; u < UN; ++u)
+                if (h + u < hi) raw[u].load(x + u * t.xs[1], at);
+#pragma unroll
+            for (int u = 0; u < UN; ++u)
+                if (h + u < hi) {
+                    float v[16];
+                    raw[u].get(v);
+                    if (at.rotated) rotary_turn_slot(v, c, s, p.interleaved);
+                    store8(y + u * t.ys[1] + at.a, v);
+                    store8(y + u * t.ys[1] + at.b, v + 8);
+                }
+            x += UN * t.xs[1];
+            y += UN * t.ys[1];
+        }
     }
 }
 
