@@ -200,14 +200,15 @@ fa_status fa_cache_append(const fa_cache_append_params *p, void *stream) {
         fa::fa_cache_append_few_kernel<<<(unsigned)blocks, 32 * fa::kFewWarps, 0, s>>>(kp);
         return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     }
-    // as many heads in a block, which share the sines, as leave every SM four blocks
-    const long long touched = (long long)c.B * kp.pages;
-    kp.group = c.H_kv;
-    while (kp.group > 1 && touched * ((c.H_kv + kp.group - 1) / kp.group) < 4LL * sms) kp.group = (kp.group + 1) / 2;
-    const long long blocks = touched * ((c.H_kv + kp.group - 1) / kp.group);
-    if (blocks > kMaxInt) return FA_ERR_INVALID_ARGUMENT;
     const int slots = c.page * (c.d / 16);  // 64 .. 2048 of 16 components
     const int threads = slots < 512 ? slots : 512;
+    // as many heads in a block, which share the sines, as leave every SM 4096 threads in all
+    const long long touched = (long long)c.B * kp.pages;
+    kp.group = c.H_kv;
+    while (kp.group > 1 && touched * ((c.H_kv + kp.group - 1) / kp.group) * threads < 4096LL * sms)
+        kp.group = (kp.group + 1) / 2;
+    const long long blocks = touched * ((c.H_kv + kp.group - 1) / kp.group);
+    if (blocks > kMaxInt) return FA_ERR_INVALID_ARGUMENT;
     switch (slots / threads) {
         case 1: launch_append<1>(kp, vec, (unsigned)blocks, threads, s); break;
         case 2: launch_append<2>(kp, vec, (unsigned)blocks, threads, s); break;

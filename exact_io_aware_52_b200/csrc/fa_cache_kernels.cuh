@@ -134,33 +134,57 @@ __device__ __forceinline__ bool touched_page(const AppendParams &p, int b, int p
     return true;
 }
 
-// A slot of 16 components of a new key (turned by cs, sn) or value in fp32; `at` says where its two
+// A slot of 16 components of a new key (turned by cs, sn) in fp32; `at` says where its two
 // runs lie.
 template <bool VEC>
-__device__ __forceinline__ void load_slot(const AppendParams &p, const uint64_t *step, const uint16_t *row, int slot,
-                                          const RotarySlot &at, int dim, int pos, const float (&cs)[8],
-                                          const float (&sn)[8], float (&v)[16]) {
+__device__ __forceinline__ void load_key(const AppendParams &p, const uint64_t *step, const uint16_t *row, int slot,
+                                         const RotarySlot &at, int pos, const float (&cs)[8], const float (&sn)[8],
+                                         float (&v)[16]) {
     if constexpr (VEC) {
         load8(row + at.a, v);
         load8(row + at.b, v + 8);
         if (at.rotated) rotary_turn_slot(v, cs, sn, p.interleaved);
     } else {
         for (int j = 0; j < 16; ++j)
-            v[j] = dim ? turned_component(p, step, row, 16 * slot + j, pos) : load1(row + 16 * slot + j);
+            v[j] = p.dim ? turned_component(p, step, row, 16 * slot + j, pos) : load1(row + 16 * slot + j);
     }
+}
+// A slot of 16 components in one piece.
+__device__ __forceinline__ RotarySlot plain_slot(int s) { return RotarySlot{16 * s, 16 * s + 8, false}; }
+// A slot of a new value as it comes: 16 bf16.
+template <bool VEC>
+__device__ __forceinline__ void load_value(const uint16_t *row, int slot, uint32_t (&w)[8]) {
+    if constexpr (VEC) {
+        const uint4 x = reinterpret_cast<const uint4 *>(row + 16 * slot)[0];
+        const uint4 y = reinterpret_cast<const uint4 *>(row + 16 * slot)[1];
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+    } else {
+        for (int j = 0; j < 8; ++j) w[j] = (uint32_t)row[16 * slot + 2 * j] | (uint32_t)row[16 * slot + 2 * j + 1] << 16;
+    }
+}
+__device__ __forceinline__ void value_floats(const uint32_t (&w)[8], float (&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[2 * j] = bf16x2_lo(w[j]), v[2 * j + 1] = bf16x2_hi(w[j]);
 }
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// Largest magnitude as bits, which order as the magnitudes do; from kInfBits on it is not finite.
-__device__ __forceinline__ uint32_t slot_amax(const float (&v)[16]) {
+// Largest magnitude as bits, which order as the magnitudes do; from kInfBits on there is an infinity
+// (or, among values, NaN).  NaN among keys is left out.
+__device__ __forceinline__ uint32_t key_amax(const float (&v)[16]) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(v[j]));
+    return __float_as_uint(m);
+}
+__device__ __forceinline__ uint32_t value_amax(const uint32_t (&w)[8]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-    return m;
+    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+    return max(m << 16, m & 0xffff0000u);
 }
 // Of the finite ones.
-__device__ __forceinline__ uint32_t slot_amax_finite(const float (&v)[16]) {
+__device__ __forceinline__ uint32_t amax_finite(const float (&v)[16]) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -231,30 +255,30 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
     for (int i = 0; i < SPT; ++i) {
         const int k = threadIdx.x + i * blockDim.x;
         const int t = k >> row_log2, slot = k & (per_row - 1);
-        at[i] = rotary_slot(slot, VEC ? dim : 0, p.interleaved);
+        at[i] = VEC ? rotary_slot(slot, c.d, dim) : plain_slot(slot);
         if (VEC && at[i].rotated && t >= pg.s0 && t < pg.s1) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                rotary_cs(step[8 * slot + j], (int)(pg.lo + t), p.amplitude, 1.f, cs[i][j], sn[i][j]);
+                rotary_cs(step[rotary_pair(slot, j, dim, p.interleaved)], (int)(pg.lo + t), p.amplitude, 1.f,
+                          cs[i][j], sn[i][j]);
         }
     }
-    const uint16_t *xk = p.x[0] + b * p.xs[0][0] + (pg.t0 - pg.s0) * p.xs[0][2];
-    const uint16_t *xv = p.x[1] + b * p.xs[1][0] + (pg.t0 - pg.s0) * p.xs[1][2];
+    const uint16_t *xk = p.x[0] + b * p.xs[0][0] + (pg.t0 - pg.s0) * p.xs[0][2] + h0 * p.xs[0][1];
+    const uint16_t *xv = p.x[1] + b * p.xs[1][0] + (pg.t0 - pg.s0) * p.xs[1][2] + h0 * p.xs[1][1];
 
-    for (int h = h0; h < h1; ++h) {
-        float k[SPT][16], v[SPT][16];
+    for (int h = h0; h < h1; ++h, xk += p.xs[0][1], xv += p.xs[1][1]) {
+        float k[SPT][16];
+        uint32_t v[SPT][8];
         uint32_t mk = 0, mv = 0;
 #pragma unroll
         for (int i = 0; i < SPT; ++i) {
             const int kk = threadIdx.x + i * blockDim.x;
             const int t = kk >> row_log2, slot = kk & (per_row - 1);
             if (t < pg.s0 || t >= pg.s1) continue;
-            const RotarySlot plain = rotary_slot(slot, 0, false);
-            load_slot<VEC>(p, step, xv + h * p.xs[1][1] + t * p.xs[1][2], slot, plain, 0, 0, cs[i], sn[i], v[i]);
-            load_slot<VEC>(p, step, xk + h * p.xs[0][1] + t * p.xs[0][2], slot, at[i], dim, (int)(pg.lo + t), cs[i], sn[i],
-                           k[i]);
-            mk = max(mk, slot_amax(k[i]));
-            mv = max(mv, slot_amax(v[i]));
+            load_value<VEC>(xv + t * p.xs[1][2], slot, v[i]);
+            load_key<VEC>(p, step, xk + t * p.xs[0][2], slot, at[i], (int)(pg.lo + t), cs[i], sn[i], k[i]);
+            mk = max(mk, key_amax(k[i]));
+            mv = max(mv, value_amax(v[i]));
         }
         uint2 *sm = s_max[h & 1];  // the other one may still be read for the head before
         auto block_max = [&]() {
@@ -262,11 +286,9 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
             mv = __reduce_max_sync(0xffffffffu, mv);
             if ((threadIdx.x & 31) == 0) sm[warp] = make_uint2(mk, mv);
             __syncthreads();
-            for (int i = 0; i < warps; ++i) {
-                const uint2 x = sm[i];
-                mk = max(mk, x.x);
-                mv = max(mv, x.y);
-            }
+            const uint2 x = sm[threadIdx.x & (warps - 1)];
+            mk = __reduce_max_sync(0xffffffffu, x.x);
+            mv = __reduce_max_sync(0xffffffffu, x.y);
         };
         const long long unit = (long long)pg.page_id * c.H_kv + h;
         // read by all before thread 0 writes them
@@ -279,8 +301,10 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
             for (int i = 0; i < SPT; ++i) {
                 const int t = (threadIdx.x + i * blockDim.x) >> row_log2;
                 if (t < pg.s0 || t >= pg.s1) continue;
-                mk = max(mk, slot_amax_finite(k[i]));
-                mv = max(mv, slot_amax_finite(v[i]));
+                float y[16];
+                value_floats(v[i], y);
+                mk = max(mk, amax_finite(k[i]));
+                mv = max(mv, amax_finite(y));
             }
             __syncthreads();
             block_max();
@@ -296,8 +320,10 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
             const int t = kk >> row_log2, slot = kk & (per_row - 1);
             if (t >= pg.s1) continue;
             if (t >= pg.s0) {
+                float y[16];
+                value_floats(v[i], y);
                 store_slot(ck + t * c.d, at[i], k[i], inv_k, special_k);
-                store_slot(cvv + t * c.d, rotary_slot(slot, 0, false), v[i], inv_v, special_v);
+                store_slot(cvv + t * c.d, plain_slot(slot), y, inv_v, special_v);
             } else {  // exact ratios for powers of two
                 if (grows_k) rescale_run(ck + t * c.d + 16 * slot, before_k * inv_k);
                 if (grows_v) rescale_run(cvv + t * c.d + 16 * slot, before_v * inv_v);
@@ -322,10 +348,11 @@ __global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(con
     if (b >= c.B) return;
     const int per_row = c.d >> 4, row_log2 = 31 - __clz(per_row);
     const int i = lane >> row_log2, slot = lane & (per_row - 1);  // new token i
-    const RotarySlot at = rotary_slot(slot, p.dim, p.interleaved), plain = rotary_slot(slot, 0, false);
+    const RotarySlot at = rotary_slot(slot, c.d, p.dim);
     float k[16], v[16];
+    uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) k[j] = v[j] = 0.f;
+    for (int j = 0; j < 16; ++j) k[j] = 0.f, w[j >> 1] = 0;
     const int start = p.start[b];
     const int n = max(0, min(p.n_new ? p.n_new[b] : p.N, p.N));
     if (i < n) {
@@ -333,15 +360,15 @@ __global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(con
         const uint16_t *xv = p.x[1] + b * p.xs[1][0] + h * p.xs[1][1] + i * p.xs[1][2];
         load8(xk + at.a, k);
         load8(xk + at.b, k + 8);
-        load8(xv + plain.a, v);
-        load8(xv + plain.b, v + 8);
+        load_value<true>(xv, slot, w);
         if (at.rotated) {
             float cs[8], sn[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) rotary_cs(p.step[8 * slot + j], start + i, p.amplitude, 1.f, cs[j], sn[j]);
+            for (int j = 0; j < 8; ++j) rotary_cs(p.step[rotary_pair(slot, j, p.dim, p.interleaved)], start + i, p.amplitude, 1.f, cs[j], sn[j]);
             rotary_turn_slot(k, cs, sn, p.interleaved);
         }
     }
+    value_floats(w, v);
     const bool first_of_seq = h == 0 && lane == 0;
     for (int pt = 0; pt < p.pages; ++pt) {
         Touched pg;
@@ -350,12 +377,12 @@ __global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(con
         const bool here = t >= pg.s0 && t < pg.s1;
         const long long unit = (long long)pg.page_id * c.H_kv + h;
         const float before_k = pg.s0 > 0 ? c.k_scale[unit] : 0.f, before_v = pg.s0 > 0 ? c.v_scale[unit] : 0.f;
-        uint32_t mk = __reduce_max_sync(0xffffffffu, here ? slot_amax(k) : 0u);
-        uint32_t mv = __reduce_max_sync(0xffffffffu, here ? slot_amax(v) : 0u);
+        uint32_t mk = __reduce_max_sync(0xffffffffu, here ? key_amax(k) : 0u);
+        uint32_t mv = __reduce_max_sync(0xffffffffu, here ? value_amax(w) : 0u);
         const bool special_k = mk >= kInfBits, special_v = mv >= kInfBits;
         if (special_k || special_v) {
-            mk = __reduce_max_sync(0xffffffffu, here ? slot_amax_finite(k) : 0u);
-            mv = __reduce_max_sync(0xffffffffu, here ? slot_amax_finite(v) : 0u);
+            mk = __reduce_max_sync(0xffffffffu, here ? amax_finite(k) : 0u);
+            mv = __reduce_max_sync(0xffffffffu, here ? amax_finite(v) : 0u);
         }
         const float now_k = fmaxf(before_k, page_scale(__uint_as_float(mk)));
         const float now_v = fmaxf(before_v, page_scale(__uint_as_float(mv)));
@@ -363,7 +390,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(con
         uint8_t *ck = c.k + unit * c.page * c.d, *cvv = c.v + unit * c.page * c.d;
         if (here) {
             store_slot(ck + t * c.d, at, k, inv_k, special_k);
-            store_slot(cvv + t * c.d, plain, v, inv_v, special_v);
+            store_slot(cvv + t * c.d, plain_slot(slot), v, inv_v, special_v);
         }
         const bool grows_k = pg.s0 > 0 && now_k != before_k, grows_v = pg.s0 > 0 && now_v != before_v;
         if (grows_k)

@@ -91,14 +91,14 @@ fa_rope_kernel(const __grid_constant__ RopeParams p) {
     const int r = threadIdx.x / slots, slot = threadIdx.x - r * slots;
     const long long row = (long long)blockIdx.x * per_block + r;
     if (r >= per_block || row >= p.rows) return;
-    const RotarySlot at = rotary_slot(slot, p.dim, p.interleaved);
+    const RotarySlot at = rotary_slot(slot, p.d, p.dim);
     if (!at.rotated && !p.copy_tail) return;
     const int b = (int)row / p.N, n = (int)row - b * p.N;
     float c[8], s[8];
     if (at.rotated) {
         const int pos = p.pos ? p.pos[b * p.pos_stride + n] : p.pos0 + n;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) rotary_cs(step[8 * slot + j], pos, p.amplitude, p.sign, c[j], s[j]);
+        for (int j = 0; j < 8; ++j) rotary_cs(step[rotary_pair(slot, j, p.dim, p.interleaved)], pos, p.amplitude, p.sign, c[j], s[j]);
     }
     constexpr int UN = 2;
     const int h0 = blockIdx.y * p.chunk, h1 = min(h0 + p.chunk, p.heads);

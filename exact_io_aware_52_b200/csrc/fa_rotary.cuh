@@ -32,20 +32,26 @@ __device__ __forceinline__ void rotary_turn(float &a, float &b, float c, float s
 
 // A head's components are handled in slots of 16: two runs of 8 components
 // that hold whole pairs, so that one thread reads, turns and writes a slot by
-// itself.  Needs d and dim to be multiples of 16.  A rotated slot s < dim / 16
-// holds the 8 pairs from 8 s: with the half layout components [8 s, 8 s + 8)
-// and the same dim / 2 further on, else [16 s, 16 s + 16).  The others pass.
+// itself.  Needs d and dim to be multiples of 16.  The runs of neighbouring slots lie
+// side by side, those of a rotated slot s < dim / 16 at 8 s and 8 s + dim / 2, those of the
+// others likewise in what is left of the head: lanes along the slots read and write
+// whole lines.  With the half layout a rotated slot has the pairs 8 s + j, with the
+// interleaved one pairs 4 s + j and dim / 4 + 4 s + j, j < 4.
 struct RotarySlot {
     int a, b;      // first component of each run
     bool rotated;
 };
-__device__ __forceinline__ RotarySlot rotary_slot(int s, int dim, bool interleaved) {
+__device__ __forceinline__ RotarySlot rotary_slot(int s, int d, int dim) {
     RotarySlot r;
     r.rotated = s < (dim >> 4);
-    const bool split = r.rotated && !interleaved;
-    r.a = split ? 8 * s : 16 * s;
-    r.b = split ? 8 * s + (dim >> 1) : 16 * s + 8;
+    const int first = r.rotated ? 0 : dim, size = r.rotated ? dim : d - dim;
+    r.a = first + 8 * (s - (first >> 4));
+    r.b = r.a + (size >> 1);
     return r;
+}
+// The pair that entry j of a rotated slot's sines and cosines belongs to.
+__device__ __forceinline__ int rotary_pair(int s, int j, int dim, bool interleaved) {
+    return interleaved ? 4 * s + (j & 3) + (j >> 2) * (dim >> 2) : 8 * s + j;
 }
 
 // Turns a slot's 16 components in place: pair j is (v[j], v[8 + j]) or (v[2 j], v[2 j + 1]).
