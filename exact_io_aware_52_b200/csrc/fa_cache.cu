@@ -69,12 +69,20 @@ bool vectors(const void *base, const int64_t *stride, int B, int H, int N) {
     return true;
 }
 
-template <int SPT>
-void launch_append(const fa::AppendParams &kp, bool vec, unsigned grid, int threads, cudaStream_t s) {
-    if (vec)
-        fa::fa_cache_append_kernel<SPT, true><<<grid, threads, 0, s>>>(kp);
-    else
-        fa::fa_cache_append_kernel<SPT, false><<<grid, threads, 0, s>>>(kp);
+template <int SPT, bool VEC>
+fa_status launch_append(const fa::AppendParams &kp, unsigned grid, int threads, int dev, cudaStream_t s) {
+    static std::atomic<bool> ready[kMaxDevices];
+    auto kern = fa::fa_cache_append_kernel<SPT, VEC>;
+    // the sines and cosines of a page's tokens: 8 bytes for each pair
+    const int smem = VEC ? kp.c.page * (kp.dim / 2) * 8 : 0;
+    if (smem > 48 * 1024 && !ready[dev].load(std::memory_order_acquire)) {
+        constexpr int most = 128 * (FA_ROTARY_MAX_DIM / 2) * 8;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+            return FA_ERR_CUDA;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    kern<<<grid, threads, smem, s>>>(kp);
+    return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------- attention
@@ -202,19 +210,19 @@ fa_status fa_cache_append(const fa_cache_append_params *p, void *stream) {
     }
     const int slots = c.page * (c.d / 16);  // 64 .. 2048 of 16 components
     const int threads = slots < 512 ? slots : 512;
-    // as many heads in a block, which share the sines, as leave every SM 4096 threads in all
+    // as many heads in a block, which share the sines, as leave every SM 2048 threads in all
     const long long touched = (long long)c.B * kp.pages;
     kp.group = c.H_kv;
-    while (kp.group > 1 && touched * ((c.H_kv + kp.group - 1) / kp.group) * threads < 4096LL * sms)
+    while (kp.group > 1 && touched * ((c.H_kv + kp.group - 1) / kp.group) * threads < 2048LL * sms)
         kp.group = (kp.group + 1) / 2;
     const long long blocks = touched * ((c.H_kv + kp.group - 1) / kp.group);
     if (blocks > kMaxInt) return FA_ERR_INVALID_ARGUMENT;
+    const unsigned grid = (unsigned)blocks;
     switch (slots / threads) {
-        case 1: launch_append<1>(kp, vec, (unsigned)blocks, threads, s); break;
-        case 2: launch_append<2>(kp, vec, (unsigned)blocks, threads, s); break;
-        default: launch_append<4>(kp, vec, (unsigned)blocks, threads, s); break;
+        case 1: return vec ? launch_append<1, true>(kp, grid, threads, dev, s) : launch_append<1, false>(kp, grid, threads, dev, s);
+        case 2: return vec ? launch_append<2, true>(kp, grid, threads, dev, s) : launch_append<2, false>(kp, grid, threads, dev, s);
+        default: return vec ? launch_append<4, true>(kp, grid, threads, dev, s) : launch_append<4, false>(kp, grid, threads, dev, s);
     }
-    return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_cache_gather(const fa_cache_gather_params *p, void *stream) {

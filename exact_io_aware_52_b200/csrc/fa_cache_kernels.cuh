@@ -86,8 +86,7 @@ __device__ __forceinline__ void values4(uint32_t w, float *v) {
 }
 
 // One component of a key, turned, for layouts that do not fall into slots.
-__device__ __forceinline__ float turned_component(const AppendParams &p, const uint64_t *step, const uint16_t *x, int e,
-                                                  int pos) {
+__device__ __forceinline__ float key_component(const AppendParams &p, const uint16_t *x, int e, int pos) {
     const float v = load1(x + e);
     if (e >= p.dim) return v;
     const int half = p.dim >> 1;
@@ -96,7 +95,7 @@ __device__ __forceinline__ float turned_component(const AppendParams &p, const u
     float a, b, c, s;
     a = first ? v : load1(x + (p.interleaved ? e - 1 : e - half));
     b = first ? load1(x + (p.interleaved ? e + 1 : e + half)) : v;
-    rotary_cs(step[i], pos, p.amplitude, 1.f, c, s);
+    rotary_cs(p.step[i], pos, p.amplitude, 1.f, c, s);
     rotary_turn(a, b, c, s);
     return first ? a : b;
 }
@@ -134,38 +133,25 @@ __device__ __forceinline__ bool touched_page(const AppendParams &p, int b, int p
     return true;
 }
 
-// A slot of 16 components of a new key (turned by cs, sn) in fp32; `at` says where its two
-// runs lie.
-template <bool VEC>
-__device__ __forceinline__ void load_key(const AppendParams &p, const uint64_t *step, const uint16_t *row, int slot,
-                                         const RotarySlot &at, int pos, const float (&cs)[8], const float (&sn)[8],
-                                         float (&v)[16]) {
-    if constexpr (VEC) {
-        load8(row + at.a, v);
-        load8(row + at.b, v + 8);
-        if (at.rotated) rotary_turn_slot(v, cs, sn, p.interleaved);
-    } else {
-        for (int j = 0; j < 16; ++j)
-            v[j] = p.dim ? turned_component(p, step, row, 16 * slot + j, pos) : load1(row + 16 * slot + j);
-    }
-}
 // A slot of 16 components in one piece.
 __device__ __forceinline__ RotarySlot plain_slot(int s) { return RotarySlot{16 * s, 16 * s + 8, false}; }
-// A slot of a new value as it comes: 16 bf16.
-template <bool VEC>
-__device__ __forceinline__ void load_value(const uint16_t *row, int slot, uint32_t (&w)[8]) {
-    if constexpr (VEC) {
-        const uint4 x = reinterpret_cast<const uint4 *>(row + 16 * slot)[0];
-        const uint4 y = reinterpret_cast<const uint4 *>(row + 16 * slot)[1];
+
+// A slot's components as they come: 16 bf16.
+struct Raw16 {
+    uint32_t w[8];
+    __device__ __forceinline__ void load(const uint16_t *row, const RotarySlot &at) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(row + at.a), y = *reinterpret_cast<const uint4 *>(row + at.b);
         w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-    } else {
-        for (int j = 0; j < 8; ++j) w[j] = (uint32_t)row[16 * slot + 2 * j] | (uint32_t)row[16 * slot + 2 * j + 1] << 16;
     }
-}
-__device__ __forceinline__ void value_floats(const uint32_t (&w)[8], float (&v)[16]) {
+    __device__ __forceinline__ void load_elements(const uint16_t *x) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[2 * j] = bf16x2_lo(w[j]), v[2 * j + 1] = bf16x2_hi(w[j]);
-}
+        for (int j = 0; j < 8; ++j) w[j] = (uint32_t)x[2 * j] | (uint32_t)x[2 * j + 1] << 16;
+    }
+    __device__ __forceinline__ void get(float (&v)[16]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[2 * j] = bf16x2_lo(w[j]), v[2 * j + 1] = bf16x2_hi(w[j]);
+    }
+};
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 
@@ -177,10 +163,10 @@ __device__ __forceinline__ uint32_t key_amax(const float (&v)[16]) {
     for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(v[j]));
     return __float_as_uint(m);
 }
-__device__ __forceinline__ uint32_t value_amax(const uint32_t (&w)[8]) {
+__device__ __forceinline__ uint32_t value_amax(const Raw16 &x) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, x.w[j] & 0x7fff7fffu);
     return max(m << 16, m & 0xffff0000u);
 }
 // Of the finite ones.
@@ -226,15 +212,18 @@ __device__ __forceinline__ void rescale_run(uint8_t *run, float ratio) {
 }
 
 // One block per (sequence, touched page, group of heads): it owns the page's codes and scales of
-// its heads, so that nothing needs atomics and no order of blocks changes the result.  A
-// thread has the same SPT slots (16 components of a token) of every head, so that the
-// sines and cosines, several times the work of the rest, are computed once for a group.
-// A head's keys and values are read once and stay in registers between the maximum
-// and the rounding.  Bound by memory: 2 bytes read and 1 written per component.
+// its heads, so that nothing needs atomics and no order of blocks changes the result.
+// The sines and cosines, several times the work of the rest, are computed once for a group
+// and lie in shared memory (registers would leave no room for the next
+// head's loads, which are in flight while a head is finished).  A head's keys and
+// values are read once and stay in registers between the maximum and the rounding; a
+// thread has the same SPT slots (16 components of a token) of every head.  Bound by
+// memory: 2 bytes read and 1 written per component.
 template <int SPT, bool VEC>
 __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
-    __shared__ uint64_t step[FA_ROTARY_MAX_DIM / 2];
+    extern __shared__ float4 s_cs[];  // [token][pair of entries][slot]: (cos, sin) of two of a slot's 8 entries
     __shared__ uint2 s_max[2][16];
+    constexpr bool AHEAD = VEC && SPT <= 2;
     const CacheView &c = p.c;
     const int groups = (c.H_kv + p.group - 1) / p.group;
     const int h0 = (blockIdx.x % groups) * p.group, h1 = min(h0 + p.group, c.H_kv);
@@ -242,44 +231,80 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
     const int pt = u % p.pages, b = u / p.pages;
     Touched pg;
     if (!touched_page(p, b, pt, threadIdx.x == 0, pg)) return;
-    const int dim = p.dim;
-    if (dim) {
-        for (int i = threadIdx.x; i < (dim >> 1); i += blockDim.x) step[i] = p.step[i];
-        __syncthreads();
-    }
+    const int dim = VEC ? p.dim : 0;
     const int per_row = c.d >> 4, row_log2 = 31 - __clz(per_row);
+    const int turned = dim >> 4;  // slots of a token that are turned
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    float cs[SPT][8], sn[SPT][8];
-    RotarySlot at[SPT];
-#pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-        const int k = threadIdx.x + i * blockDim.x;
-        const int t = k >> row_log2, slot = k & (per_row - 1);
-        at[i] = VEC ? rotary_slot(slot, c.d, dim) : plain_slot(slot);
-        if (VEC && at[i].rotated && t >= pg.s0 && t < pg.s1) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                rotary_cs(step[rotary_pair(slot, j, dim, p.interleaved)], (int)(pg.lo + t), p.amplitude, 1.f,
-                          cs[i][j], sn[i][j]);
-        }
-    }
     const uint16_t *xk = p.x[0] + b * p.xs[0][0] + (pg.t0 - pg.s0) * p.xs[0][2] + h0 * p.xs[0][1];
     const uint16_t *xv = p.x[1] + b * p.xs[1][0] + (pg.t0 - pg.s0) * p.xs[1][2] + h0 * p.xs[1][1];
 
-    for (int h = h0; h < h1; ++h, xk += p.xs[0][1], xv += p.xs[1][1]) {
+    Raw16 rk[SPT], rv[SPT];
+    // This thread's slots of the head at xk, xv.
+    auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < SPT; ++i) {
+            const int kk = threadIdx.x + i * blockDim.x;
+            const int t = kk >> row_log2, slot = kk & (per_row - 1);
+            if (t < pg.s0 || t >= pg.s1) continue;
+            if constexpr (VEC) {
+                rk[i].load(xk + t * p.xs[0][2], rotary_slot(slot, c.d, dim));
+                rv[i].load(xv + t * p.xs[1][2], plain_slot(slot));
+            } else {
+                rv[i].load_elements(xv + t * p.xs[1][2] + 16 * slot);
+            }
+        }
+    };
+    load();
+    if constexpr (VEC) {
+        if (dim) {
+            __shared__ uint64_t step[FA_ROTARY_MAX_DIM / 2];
+            for (int i = threadIdx.x; i < (dim >> 1); i += blockDim.x) step[i] = p.step[i];
+            __syncthreads();
+            const unsigned n = (pg.s1 - pg.s0) * 4 * turned;
+            for (unsigned k = threadIdx.x; k < n; k += blockDim.x) {
+                const unsigned q = k / (unsigned)turned, slot = k - q * turned;
+                const int t = pg.s0 + (q >> 2), j = 2 * (q & 3);
+                float4 x;
+                rotary_cs(step[rotary_pair(slot, j, dim, p.interleaved)], (int)(pg.lo + t), p.amplitude, 1.f, x.x, x.y);
+                rotary_cs(step[rotary_pair(slot, j + 1, dim, p.interleaved)], (int)(pg.lo + t), p.amplitude, 1.f, x.z, x.w);
+                s_cs[(t * 4 + (q & 3)) * turned + slot] = x;
+            }
+            __syncthreads();
+        }
+    }
+
+    for (int h = h0; h < h1; ++h) {
+        if (!AHEAD && h > h0) load();
         float k[SPT][16];
-        uint32_t v[SPT][8];
+        Raw16 v[SPT];
         uint32_t mk = 0, mv = 0;
 #pragma unroll
         for (int i = 0; i < SPT; ++i) {
             const int kk = threadIdx.x + i * blockDim.x;
             const int t = kk >> row_log2, slot = kk & (per_row - 1);
             if (t < pg.s0 || t >= pg.s1) continue;
-            load_value<VEC>(xv + t * p.xs[1][2], slot, v[i]);
-            load_key<VEC>(p, step, xk + t * p.xs[0][2], slot, at[i], (int)(pg.lo + t), cs[i], sn[i], k[i]);
+            v[i] = rv[i];
+            if constexpr (VEC) {
+                rk[i].get(k[i]);
+                if (slot < turned) {
+                    float cs[8], sn[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 x = s_cs[(t * 4 + j) * turned + slot];
+                        cs[2 * j] = x.x, sn[2 * j] = x.y, cs[2 * j + 1] = x.z, sn[2 * j + 1] = x.w;
+                    }
+                    rotary_turn_slot(k[i], cs, sn, p.interleaved);
+                }
+            } else {
+                for (int j = 0; j < 16; ++j)
+                    k[i][j] = key_component(p, xk + t * p.xs[0][2], 16 * slot + j, (int)(pg.lo + t));
+            }
             mk = max(mk, key_amax(k[i]));
             mv = max(mv, value_amax(v[i]));
         }
+        xk += p.xs[0][1];
+        xv += p.xs[1][1];
+        if (AHEAD && h + 1 < h1) load();
         uint2 *sm = s_max[h & 1];  // the other one may still be read for the head before
         auto block_max = [&]() {
             mk = __reduce_max_sync(0xffffffffu, mk);
@@ -302,7 +327,7 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
                 const int t = (threadIdx.x + i * blockDim.x) >> row_log2;
                 if (t < pg.s0 || t >= pg.s1) continue;
                 float y[16];
-                value_floats(v[i], y);
+                v[i].get(y);
                 mk = max(mk, amax_finite(k[i]));
                 mv = max(mv, amax_finite(y));
             }
@@ -321,8 +346,8 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
             if (t >= pg.s1) continue;
             if (t >= pg.s0) {
                 float y[16];
-                value_floats(v[i], y);
-                store_slot(ck + t * c.d, at[i], k[i], inv_k, special_k);
+                v[i].get(y);
+                store_slot(ck + t * c.d, VEC ? rotary_slot(slot, c.d, dim) : plain_slot(slot), k[i], inv_k, special_k);
                 store_slot(cvv + t * c.d, plain_slot(slot), y, inv_v, special_v);
             } else {  // exact ratios for powers of two
                 if (grows_k) rescale_run(ck + t * c.d + 16 * slot, before_k * inv_k);
@@ -350,9 +375,9 @@ __global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(con
     const int i = lane >> row_log2, slot = lane & (per_row - 1);  // new token i
     const RotarySlot at = rotary_slot(slot, c.d, p.dim);
     float k[16], v[16];
-    uint32_t w[8];
+    Raw16 w;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) k[j] = 0.f, w[j >> 1] = 0;
+    for (int j = 0; j < 16; ++j) k[j] = 0.f, w.w[j >> 1] = 0;
     const int start = p.start[b];
     const int n = max(0, min(p.n_new ? p.n_new[b] : p.N, p.N));
     if (i < n) {
@@ -360,7 +385,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(con
         const uint16_t *xv = p.x[1] + b * p.xs[1][0] + h * p.xs[1][1] + i * p.xs[1][2];
         load8(xk + at.a, k);
         load8(xk + at.b, k + 8);
-        load_value<true>(xv, slot, w);
+        w.load(xv, plain_slot(slot));
         if (at.rotated) {
             float cs[8], sn[8];
 #pragma unroll
@@ -368,7 +393,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(con
             rotary_turn_slot(k, cs, sn, p.interleaved);
         }
     }
-    value_floats(w, v);
+    w.get(v);
     const bool first_of_seq = h == 0 && lane == 0;
     for (int pt = 0; pt < p.pages; ++pt) {
         Touched pg;
