@@ -9,8 +9,8 @@ library returns raises FaError; neither launches anything.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import struct
 
 import torch
 
@@ -20,49 +20,72 @@ _LAYOUTS = {"half": fb.FA_ROTARY_HALF, "interleaved": fb.FA_ROTARY_INTERLEAVED}
 _SCALINGS = {"none": fb.FA_ROTARY_NONE, "linear": fb.FA_ROTARY_LINEAR, "base": fb.FA_ROTARY_BASE,
              "parts": fb.FA_ROTARY_PARTS}
 _DTYPES = {torch.bfloat16: fb.FA_T_BF16, torch.float32: fb.FA_T_F32}
-_I3 = ctypes.c_int64 * 3
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream
+
+# A decoding step makes several of these calls for kernels of a few microseconds, so the parameter
+# structures are packed in one go (filling a ctypes.Structure takes several times as long).
+_TENSOR = "PPi3q3q"
+_ROPE = struct.Struct("@" + _TENSOR + _TENSOR + "iiiiiPqiiP")
+_CACHE = struct.Struct("@PPPPPqiiiiii")
+_APPEND = struct.Struct("@PP3q3qiPPPP")      # what follows the cache
+_GATHER = struct.Struct("@PPPiP")
+_ATTN = struct.Struct("@PPPPPiiifiPNIi")
+for _s, _c, _rest in ((_ROPE, fb.FaRopeParams, 0), (_CACHE, fb.FaCache, 0), (_APPEND, fb.FaCacheAppendParams, _CACHE.size),
+                      (_GATHER, fb.FaCacheGatherParams, _CACHE.size), (_ATTN, fb.FaCacheAttnParams, _CACHE.size)):
+    assert _s.size + _rest == ctypes.sizeof(_c), _c.__name__
+_calls = {}
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _call(name):
+    """The library's function, taking a packed structure."""
+    f = _calls.get(name)
+    if f is None:
+        f = fb.load()[name]
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+        _calls[name] = f
+    return f
 
 
-def _device_of(t, name):
-    _need(t.is_cuda, f"{name} must be a CUDA tensor")
-    return t.get_device()
+def _refuse(what):
+    raise ValueError(what)
 
 
-def _ints(t, name, shape, dev):
-    """The address of an int32 tensor of this shape on this device; None passes."""
+def _pack(form, *values):
+    try:
+        return form.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"an argument is not a number of its range: {e}") from None
+
+
+def _ints(t, name, size, dev):
+    """The address of an int32 tensor of this size on this device; 0 for None."""
     if t is None:
-        return None
-    _need(t.dtype == torch.int32 and tuple(t.shape) == shape and t.get_device() == dev and t.is_contiguous(),
-          f"{name} must be a contiguous int32 tensor of shape {shape} on the same device")
+        return 0
+    if t.dtype is not _I32 or t.dim() != 1 or t.shape[0] != size or t.get_device() != dev or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous int32 tensor of {size} on the same device")
     return t.data_ptr()
 
 
-@contextlib.contextmanager
+def _heads(t, name, dev):
+    if t.dim() != 4 or t.get_device() != dev or dev < 0:
+        _refuse(f"{name} must be a CUDA tensor [B, heads, N, d], all on the same device")
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] > 1:
+        _refuse(f"{name}: the components of a head must be contiguous")
+    return st
+
+
 def _elsewhere(dev, stream):
     """The given device and stream as the current ones, so that tensors allocated
-    meanwhile belong to that stream."""
-    with torch.cuda.device(dev):
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(dev)
-        with torch.cuda.stream(stream):
-            yield
-
-
-def _run(dev, stream, call, *args):
-    """call(*args) with `dev` and `stream` current."""
-    if stream is None and dev == torch.cuda.current_device():
-        return call(*args)
-    with _elsewhere(dev, stream):
-        return call(*args)
-
-
-def _raw_stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+    meanwhile belong to that stream; None if they are that already."""
+    if stream is None:
+        return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
 
 
 class Rotary:
@@ -80,26 +103,25 @@ class Rotary:
 
     def __init__(self, dim, layout="half", base=10000.0, scaling="none", factor=1.0, original_length=0.0,
                  low_turns=1.0, high_turns=32.0, amplitude=1.0, angles=None):
-        _need(layout in _LAYOUTS, f"layout must be one of {sorted(_LAYOUTS)}")
-        _need(scaling in _SCALINGS, f"scaling must be one of {sorted(_SCALINGS)}")
-        _need(amplitude > 0.0, "amplitude must be positive")
+        if layout not in _LAYOUTS:
+            _refuse(f"layout must be one of {sorted(_LAYOUTS)}")
+        if scaling not in _SCALINGS:
+            _refuse(f"scaling must be one of {sorted(_SCALINGS)}")
+        if not amplitude > 0.0:
+            _refuse("amplitude must be positive")
         spec = fb.FaRotarySpec(dim=int(dim), layout=_LAYOUTS[layout], base=float(base), scaling=_SCALINGS[scaling],
                                factor=float(factor), original_length=float(original_length),
                                low_turns=float(low_turns), high_turns=float(high_turns), amplitude=float(amplitude))
         if angles is not None:
             own = [float(a) for a in angles]
-            _need(len(own) == int(dim) // 2, "angles must have one entry for each of the dim / 2 pairs")
+            if len(own) != int(dim) // 2:
+                _refuse("angles must have one entry for each of the dim / 2 pairs")
             spec.angles = (ctypes.c_double * len(own))(*own)
         self.struct = fb.FaRotary()
         fb._check(fb.load().fa_rotary_init(ctypes.byref(self.struct), ctypes.byref(spec)), "fa_rotary_init")
         self.dim = int(dim)
         self.layout = layout
-        self._ref = ctypes.pointer(self.struct)
-
-
-def _head_tensor(t, name):
-    _need(t.dim() == 4, f"{name} must be [B, heads, N, d]")
-    _need(t.shape[3] <= 1 or t.stride(3) == 1, f"{name}: the components of a head must be contiguous")
+        self._address = ctypes.addressof(self.struct)
 
 
 def rope(rotary, q, k=None, *, pos=None, pos0=0, inverse=False, out_dtype=None, out=None, stream=None):
@@ -112,59 +134,67 @@ def rope(rotary, q, k=None, *, pos=None, pos0=0, inverse=False, out_dtype=None, 
     or a pair with k.  out: a tensor (or a pair) to write instead, any strides; the inputs
     themselves turn in place.  They must not overlap the inputs otherwise.
     """
-    dev = _device_of(q, "q")
-    _need(isinstance(rotary, Rotary), "rotary must be a Rotary")
-    _head_tensor(q, "q")
+    dev = q.get_device()
+    if not isinstance(rotary, Rotary):
+        _refuse("rotary must be a Rotary")
+    sq = _heads(q, "q", dev)
     B, H, N, d = q.shape
+    x_type = _DTYPES.get(q.dtype)
     if k is not None:
-        _head_tensor(k, "k")
-        _need(k.shape[0] == B and k.shape[2] == N and k.shape[3] == d and k.dtype == q.dtype and k.get_device() == dev,
-              "k must be [B, H_kv, N, d] of q's dtype and on its device")
+        sk = _heads(k, "k", dev)
+        Bk, Hk, Nk, dk = k.shape
+        if Bk != B or Nk != N or dk != d or k.dtype is not q.dtype:
+            _refuse("k must be [B, H_kv, N, d] of q's dtype")
     if out is None:
-        _need(q.dtype in _DTYPES and (out_dtype is None or out_dtype in _DTYPES), "dtypes must be bf16 or fp32")
-        y_type = out_dtype or q.dtype
-        outs = None
+        yq = yk = None
+        y_dtype = q.dtype if out_dtype is None else out_dtype
     else:
-        outs = tuple(out) if k is not None else (out,)
-        y_type = outs[0].dtype
-        for x, y, name in zip((q, k), outs, ("out of q", "out of k")):
-            _head_tensor(y, name)
-            _need(y.shape == x.shape and y.get_device() == dev and y.dtype == y_type,
-                  f"{name} must have its input's shape and device, and both the same dtype")
-        _need(q.dtype in _DTYPES and y_type in _DTYPES and (out_dtype is None or out_dtype == y_type),
-              "dtypes must be bf16 or fp32, and out of out_dtype")
-    pos_stride = 0
+        yq, yk = (out, None) if k is None else out
+        y_dtype = yq.dtype
+        for x, y in ((q, yq), (k, yk)):
+            if x is not None:
+                _heads(y, "out", dev)
+                if y.shape != x.shape or y.dtype is not y_dtype:
+                    _refuse("out must have its input's shape, and both the same dtype")
+        if out_dtype is not None and out_dtype is not y_dtype:
+            _refuse("out must be of out_dtype")
+    y_type = _DTYPES.get(y_dtype)
+    if x_type is None or y_type is None:
+        _refuse("dtypes must be bf16 or fp32")
+    pos_at = pos_stride = 0
     if pos is not None:
-        _need(pos.dtype == torch.int32 and pos.get_device() == dev and pos.shape[-1:] == (N,) and
-              (pos.dim() == 1 or (pos.dim() == 2 and pos.shape[0] == B)) and (N <= 1 or pos.stride(-1) == 1),
-              "pos must be int32 [B, N] or [N] on the same device, contiguous along the tokens")
-        pos_stride = pos.stride(0) if pos.dim() == 2 else 0
-    return _run(dev, stream, _rope, rotary, q, k, outs, y_type, pos, pos_stride, int(pos0), int(bool(inverse)), dev)
+        sp = pos.shape
+        if (pos.dtype is not _I32 or pos.get_device() != dev or len(sp) not in (1, 2) or sp[-1] != N or
+                (len(sp) == 2 and sp[0] != B) or (N > 1 and pos.stride(-1) != 1)):
+            _refuse("pos must be int32 [B, N] or [N] on the same device, contiguous along the tokens")
+        pos_at = pos.data_ptr()
+        pos_stride = pos.stride(0) if len(sp) == 2 else 0
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return rope(rotary, q, k, pos=pos, pos0=pos0, inverse=inverse, out_dtype=out_dtype, out=out)
 
-
-def _rope(rotary, q, k, outs, y_type, pos, pos_stride, pos0, inverse, dev):
-    B, H, N, d = q.shape
-    if outs is None:
-        outs = (torch.empty((B, H, N, d), dtype=y_type, device=q.device),)
-        if k is not None:
-            outs += (torch.empty(k.shape, dtype=y_type, device=q.device),)
-    p = fb.FaRopeParams()
-    for t, x, y in zip(p.t, (q, k), outs):
-        t.x = x.data_ptr()
-        t.y = y.data_ptr()
-        t.heads = x.shape[1]
-        t.x_stride[:] = x.stride()[:3]
-        t.y_stride[:] = y.stride()[:3]
-    p.B, p.N, p.d = B, N, d
-    p.x_dtype, p.y_dtype = _DTYPES[q.dtype], _DTYPES[y_type]
-    if pos is not None:
-        p.pos = pos.data_ptr()
-        p.pos_stride = pos_stride
-    p.pos0 = pos0
-    p.inverse = inverse
-    p.rotary = rotary._ref
-    fb._check(fb.load().fa_rope(p, _raw_stream(dev)), "fa_rope")
-    return outs if k is not None else outs[0]
+    c1, c2 = N * d, H * N * d
+    if yq is None:
+        # like q, its strides too, where those are the contiguous ones
+        yq = torch.empty_like(q) if sq == (c2, c1, d, 1) and y_dtype is q.dtype else q.new_empty((B, H, N, d), dtype=y_dtype)
+    syq = yq.stride()
+    if k is None:
+        p = _pack(_ROPE, q.data_ptr(), yq.data_ptr(), H, sq[0], sq[1], sq[2], syq[0], syq[1], syq[2],
+                       0, 0, 0, 0, 0, 0, 0, 0, 0,
+                       B, N, d, x_type, y_type, pos_at, pos_stride, pos0, 1 if inverse else 0, rotary._address)
+    else:
+        if yk is None:
+            yk = torch.empty_like(k) if sk == (Hk * c1, c1, d, 1) and y_dtype is q.dtype else \
+                k.new_empty((B, Hk, N, d), dtype=y_dtype)
+        syk = yk.stride()
+        p = _pack(_ROPE, q.data_ptr(), yq.data_ptr(), H, sq[0], sq[1], sq[2], syq[0], syq[1], syq[2],
+                       k.data_ptr(), yk.data_ptr(), Hk, sk[0], sk[1], sk[2], syk[0], syk[1], syk[2],
+                       B, N, d, x_type, y_type, pos_at, pos_stride, pos0, 1 if inverse else 0, rotary._address)
+    st = _call("fa_rope")(p, _raw_stream(dev))
+    if st:
+        raise fb.FaError(st, "fa_rope")
+    return yq if k is None else (yq, yk)
 
 
 class PagedCache:
@@ -178,25 +208,27 @@ class PagedCache:
     """
 
     def __init__(self, k, v, k_scale, v_scale, table):
-        dev = _device_of(k, "k")
-        _need(k.dim() == 4 and k.shape == v.shape, "k and v must be [n_pages, H_kv, page, d]")
+        dev = k.get_device()
+        if dev < 0 or k.dim() != 4 or k.shape != v.shape:
+            _refuse("k and v must be CUDA tensors [n_pages, H_kv, page, d]")
         for t, name in ((k, "k"), (v, "v")):
-            _need(t.dtype in (torch.float8_e4m3fn, torch.uint8) and t.is_contiguous() and t.get_device() == dev,
-                  f"{name} must be a contiguous float8_e4m3fn (or uint8) tensor on the same device")
+            if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or not t.is_contiguous() or t.get_device() != dev:
+                _refuse(f"{name} must be a contiguous float8_e4m3fn (or uint8) tensor on the same device")
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _need(t.dtype == torch.float32 and t.shape == k.shape[:2] and t.is_contiguous() and t.get_device() == dev,
-                  f"{name} must be a contiguous fp32 [n_pages, H_kv] tensor on the same device")
-        _need(table.dtype == torch.int32 and table.dim() == 2 and table.get_device() == dev and
-              (table.shape[1] <= 1 or table.stride(1) == 1),
-              "table must be int32 [B, max_pages] on the same device, contiguous along the pages")
+            if t.dtype is not _F32 or t.shape != k.shape[:2] or not t.is_contiguous() or t.get_device() != dev:
+                _refuse(f"{name} must be a contiguous fp32 [n_pages, H_kv] tensor on the same device")
+        if (table.dtype is not _I32 or table.dim() != 2 or table.get_device() != dev or
+                (table.shape[1] > 1 and table.stride(1) != 1)):
+            _refuse("table must be int32 [B, max_pages] on the same device, contiguous along the pages")
         self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
         self.device_index = dev
         self.n_pages, self.H_kv, self.page, self.d = k.shape
         self.B, self.max_pages = table.shape
-        self.struct = fb.FaCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
-                                 table.stride(0), self.n_pages, self.max_pages, self.B, self.H_kv, self.page, self.d)
-        _need(self.page in (16, 32, 64, 128) and self.d in (64, 128, 256),
-              "page must be 16, 32, 64 or 128 and d 64, 128 or 256")
+        if self.page not in (16, 32, 64, 128) or self.d not in (64, 128, 256):
+            _refuse("page must be 16, 32, 64 or 128 and d 64, 128 or 256")
+        self._packed = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                   table.data_ptr(), table.stride(0), self.n_pages, self.max_pages, self.B, self.H_kv,
+                                   self.page, self.d)
         self._workspace = {}  # (H, N) -> bytes
 
 
@@ -209,22 +241,28 @@ def cache_append(cache, k, v, start, *, n_new=None, rotary=None, dev_status=None
     positions on the way.  dev_status: int32 status word for FA_ERR_BAD_PAGE.
     """
     dev = cache.device_index
-    for t, name in ((k, "k"), (v, "v")):
-        _head_tensor(t, name)
-        _need(t.dtype == torch.bfloat16 and t.get_device() == dev, f"{name} must be bf16 on the cache's device")
-    N = k.shape[2]
-    _need(tuple(k.shape) == (cache.B, cache.H_kv, N, cache.d) and v.shape == k.shape,
-          f"k and v must be [{cache.B}, {cache.H_kv}, N, {cache.d}]")
-    _need(rotary is None or isinstance(rotary, Rotary), "rotary must be a Rotary")
-    p = fb.FaCacheAppendParams(
-        cache.struct, k.data_ptr(), v.data_ptr(), _I3(*k.stride()[:3]), _I3(*v.stride()[:3]), N,
-        _ints(start, "start", (cache.B,), dev), _ints(n_new, "n_new", (cache.B,), dev),
-        None if rotary is None else rotary._ref, _ints(dev_status, "dev_status", (1,), dev))
-    _run(dev, stream, _append, p, dev)
-
-
-def _append(p, dev):
-    fb._check(fb.load().fa_cache_append(p, _raw_stream(dev)), "fa_cache_append")
+    sk, sv = _heads(k, "k", dev), _heads(v, "v", dev)
+    B, H, N, d = k.shape
+    if B != cache.B or H != cache.H_kv or d != cache.d or v.shape != k.shape:
+        _refuse(f"k and v must be [{cache.B}, {cache.H_kv}, N, {cache.d}]")
+    if k.dtype is not _BF16 or v.dtype is not _BF16:
+        _refuse("k and v must be bf16")
+    if rotary is not None and not isinstance(rotary, Rotary):
+        _refuse("rotary must be a Rotary")
+    if start is None:
+        _refuse("start must be given")
+    p = cache._packed + _pack(
+        _APPEND, k.data_ptr(), v.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], N,
+        _ints(start, "start", B, dev), _ints(n_new, "n_new", B, dev), 0 if rotary is None else rotary._address,
+        _ints(dev_status, "dev_status", 1, dev))
+    there = _elsewhere(dev, stream)
+    if there is None:
+        st = _call("fa_cache_append")(p, _raw_stream(dev))
+    else:
+        with there:
+            st = _call("fa_cache_append")(p, _raw_stream(dev))
+    if st:
+        raise fb.FaError(st, "fa_cache_append")
 
 
 def cache_gather(cache, k_len, N_k, *, out=None, dev_status=None, stream=None):
@@ -233,30 +271,39 @@ def cache_gather(cache, k_len, N_k, *, out=None, dev_status=None, stream=None):
     attention(..., k_len=k_len) reads.  out: a pair of such tensors to write."""
     dev = cache.device_index
     N_k = int(N_k)
-    _need(N_k >= 0, "N_k must not be negative")
+    if N_k < 0:
+        _refuse("N_k must not be negative")
     shape = (cache.B, cache.H_kv, N_k, cache.d)
     if out is not None:
         for t in out:
-            _need(t.dtype == torch.bfloat16 and tuple(t.shape) == shape and t.is_contiguous() and
-                  t.get_device() == dev, f"out must be two contiguous bf16 tensors of shape {shape}")
-    return _run(dev, stream, _gather, cache, _ints(k_len, "k_len", (cache.B,), dev), shape, out,
-                _ints(dev_status, "dev_status", (1,), dev), dev)
-
-
-def _gather(cache, k_len, shape, out, dev_status, dev):
+            if t.dtype is not _BF16 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+                _refuse(f"out must be two contiguous bf16 tensors of shape {shape}")
+    if k_len is None:
+        _refuse("k_len must be given")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return cache_gather(cache, k_len, N_k, out=out, dev_status=dev_status)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) for _ in range(2))
-    p = fb.FaCacheGatherParams(cache.struct, k_len, out[0].data_ptr(), out[1].data_ptr(), shape[2], dev_status)
-    fb._check(fb.load().fa_cache_gather(p, _raw_stream(dev)), "fa_cache_gather")
-    return tuple(out)
+        ref = cache.k_scale
+        out = (ref.new_empty(shape, dtype=_BF16), ref.new_empty(shape, dtype=_BF16))
+    k, v = out
+    p = cache._packed + _pack(_GATHER, _ints(k_len, "k_len", cache.B, dev), k.data_ptr(), v.data_ptr(), N_k,
+                                     _ints(dev_status, "dev_status", 1, dev))
+    st = _call("fa_cache_gather")(p, _raw_stream(dev))
+    if st:
+        raise fb.FaError(st, "fa_cache_gather")
+    return k, v
 
 
 def cache_attention_workspace_bytes(cache, H, N):
     """Scratch bytes that cache_attention needs for H query heads and N query tokens."""
     size = cache._workspace.get((H, N))
     if size is None:
-        p = fb.FaCacheAttnParams(cache=cache.struct, H=H, N=N)
-        size = cache._workspace[(H, N)] = int(fb.load().fa_cache_attn_workspace_bytes(ctypes.byref(p)))
+        f = fb.load()["fa_cache_attn_workspace_bytes"]
+        f.restype = ctypes.c_size_t
+        f.argtypes = [ctypes.c_char_p]
+        size = cache._workspace[(H, N)] = f(cache._packed + _pack(_ATTN, 0, 0, 0, 0, 0, H, N, 0, 0.0, 0, 0, 0, 0, 0))
     return size
 
 
@@ -273,37 +320,46 @@ def cache_attention(cache, q, k_len, causal, scale, *, out_dtype=None, out=None,
     word for FA_ERR_BAD_PAGE and FA_ERR_DEVICE_TIMEOUT (a wait longer than timeout_ms, 0 = 2000).
     """
     dev = cache.device_index
-    _need(q.dim() == 4 and q.dtype == torch.bfloat16 and q.is_contiguous() and q.get_device() == dev,
-          "q must be a contiguous bf16 [B, H, N, d] tensor on the cache's device")
+    if q.dim() != 4 or q.dtype is not _BF16 or not q.is_contiguous() or q.get_device() != dev:
+        _refuse("q must be a contiguous bf16 [B, H, N, d] tensor on the cache's device")
     B, H, N, d = q.shape
-    _need(B == cache.B and d == cache.d, f"q must be [{cache.B}, H, N, {cache.d}]")
-    _need(cache.H_kv == 0 or H % cache.H_kv == 0, "H must be a multiple of the cache's heads")
-    o_type = out_dtype or torch.float32
-    if out is not None:
-        o, lse = out
-        o_type = o.dtype
-        _need(o.shape == q.shape and o.is_contiguous() and o.get_device() == dev and lse.dtype == torch.float32 and
-              lse.shape == q.shape[:3] and lse.is_contiguous() and lse.get_device() == dev and
-              (out_dtype is None or out_dtype == o_type),
-              "out must be a contiguous O of q's shape and an fp32 lse [B, H, N] on the same device")
-    _need(o_type in _DTYPES, "out_dtype must be bf16 or fp32")
-    if workspace is not None:
-        _need(workspace.is_contiguous() and workspace.get_device() == dev,
-              "workspace must be contiguous and on the same device")
-    return _run(dev, stream, _attention, cache, q, _ints(k_len, "k_len", (B,), dev), int(bool(causal)), float(scale),
-                out, o_type, workspace, _ints(dev_status, "dev_status", (1,), dev), timeout_ms, test_drop_load, dev)
-
-
-def _attention(cache, q, k_len, causal, scale, out, o_type, workspace, dev_status, timeout_ms, test_drop_load, dev):
-    B, H, N, d = q.shape
+    if B != cache.B or d != cache.d:
+        _refuse(f"q must be [{cache.B}, H, N, {cache.d}]")
+    if cache.H_kv and H % cache.H_kv:
+        _refuse("H must be a multiple of the cache's heads")
     if out is None:
-        out = (torch.empty((B, H, N, d), dtype=o_type, device=q.device),
-               torch.empty((B, H, N), dtype=torch.float32, device=q.device))
+        o_dtype = _F32 if out_dtype is None else out_dtype
+    else:
+        o, lse = out
+        o_dtype = o.dtype
+        if (o.shape != q.shape or not o.is_contiguous() or o.get_device() != dev or lse.dtype is not _F32 or
+                lse.shape != q.shape[:3] or not lse.is_contiguous() or lse.get_device() != dev or
+                (out_dtype is not None and out_dtype is not o_dtype)):
+            _refuse("out must be a contiguous O of q's shape and an fp32 lse [B, H, N] on the same device")
+    if o_dtype is not _BF16 and o_dtype is not _F32:
+        _refuse("out_dtype must be bf16 or fp32")
+    if workspace is not None and (not workspace.is_contiguous() or workspace.get_device() != dev):
+        _refuse("workspace must be contiguous and on the same device")
+    if k_len is None:
+        _refuse("k_len must be given")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return cache_attention(cache, q, k_len, causal, scale, out_dtype=out_dtype, out=out, workspace=workspace,
+                                   dev_status=dev_status, timeout_ms=timeout_ms, test_drop_load=test_drop_load)
+    if out is None:
+        o = torch.empty_like(q) if o_dtype is _BF16 else q.new_empty(q.shape, dtype=_F32)
+        lse = q.new_empty((B, H, N), dtype=_F32)
     if workspace is None:
-        workspace = torch.empty(cache_attention_workspace_bytes(cache, H, N), dtype=torch.uint8, device=q.device)
-    p = fb.FaCacheAttnParams(cache.struct, q.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), k_len, dev_status, H, N,
-                             causal, scale, fb.FA_O_BF16 if o_type == torch.bfloat16 else fb.FA_O_F32,
-                             workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), timeout_ms, test_drop_load)
-    fb._check(fb.load().fa_cache_attn(p, _raw_stream(dev)), "fa_cache_attn")
-    return tuple(out)
+        size = cache_attention_workspace_bytes(cache, H, N)
+        workspace = q.new_empty(size, dtype=torch.uint8)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    p = cache._packed + _pack(
+        _ATTN, q.data_ptr(), o.data_ptr(), lse.data_ptr(), _ints(k_len, "k_len", B, dev), _ints(dev_status, "dev_status", 1, dev),
+        H, N, 1 if causal else 0, scale, fb.FA_O_BF16 if o_dtype is _BF16 else fb.FA_O_F32, workspace.data_ptr(), size,
+        timeout_ms, test_drop_load)
+    st = _call("fa_cache_attn")(p, _raw_stream(dev))
+    if st:
+        raise fb.FaError(st, "fa_cache_attn")
+    return o, lse

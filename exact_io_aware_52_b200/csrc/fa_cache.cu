@@ -116,6 +116,9 @@ AttnPlan plan_attn(const fa_cache_attn_params *p, int resident) {
     return a;
 }
 
+// Up to this many tokens a sequence can hold, one CTA takes a (sequence, head) pair whole.
+constexpr int kDirectTokens = 1024;
+
 bool attn_empty(const fa_cache_attn_params *p) {
     return p->cache.B == 0 || p->cache.H_kv == 0 || p->H == 0 || p->N == 0;
 }
@@ -137,20 +140,35 @@ fa_status launch_merge(const fa::cattn::Params &kp, int nt8, cudaStream_t s) {
                                                                                                        : FA_ERR_CUDA;
 }
 
+template <int D, int NT, int WARPS>
+fa_status set_attn_smem(int dev) {
+    static std::atomic<bool> ready[kMaxDevices];
+    if (ready[dev].load(std::memory_order_acquire)) return FA_OK;
+    if (cudaFuncSetAttribute(fa::cattn::fa_cache_attn_kernel<D, NT, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             fa::cattn::kSmemBytes<D, WARPS>) != cudaSuccess)
+        return FA_ERR_CUDA;
+    ready[dev].store(true, std::memory_order_release);
+    return FA_OK;
+}
+
 template <int D, int NT>
 fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_t s) {
     namespace ca = fa::cattn;
-    static std::atomic<bool> ready[kMaxDevices];
-    auto kern = ca::fa_cache_attn_kernel<D, NT>;
-    if (!ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ca::kSmemBytes<D>) != cudaSuccess)
-            return FA_ERR_CUDA;
-        ready[dev].store(true, std::memory_order_release);
+    if ((long long)kp.c.max_pages * kp.c.page <= kDirectTokens && (long long)kp.c.B * kp.c.H_kv * kp.chunks <= sms) {
+        constexpr int W = ca::kDirectWarps<D, NT>;
+        const fa_status st = set_attn_smem<D, NT, W>(dev);
+        if (st != FA_OK) return st;
+        ca::fa_cache_attn_kernel<D, NT, W>
+            <<<kp.c.B * kp.c.H_kv * kp.chunks, 32 * W, ca::kSmemBytes<D, W>, s>>>(kp);
+        return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     }
+    const fa_status st = set_attn_smem<D, NT, ca::kWarps>(dev);
+    if (st != FA_OK) return st;
     // few workers are spread over the SMs, one warp in a CTA at work
     const int warps = kp.chunks * kp.workers, ctas = ca::kResident<D, NT> * sms;
     const int full = (warps + ca::kWarps - 1) / ca::kWarps;
-    kern<<<full > ctas ? full : (warps < ctas ? warps : ctas), ca::kThreads, ca::kSmemBytes<D>, s>>>(kp);
+    ca::fa_cache_attn_kernel<D, NT, ca::kWarps>
+        <<<full > ctas ? full : (warps < ctas ? warps : ctas), 32 * ca::kWarps, ca::kSmemBytes<D, ca::kWarps>, s>>>(kp);
     if (cudaPeekAtLastError() != cudaSuccess) return FA_ERR_CUDA;
 
     // The merge is launched while the first kernel runs and waits in it for its results.  A pair

@@ -39,8 +39,10 @@
 namespace fa {
 namespace cattn {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 4;         // of a CTA when the keys are split
+// Of a CTA that takes a whole pair: as many as its registers and rings allow, since one warp for
+// each scheduler takes 0.9 us for a tile, which more warps hide.
+template <int D, int NT> constexpr int kDirectWarps = D <= 128 && NT == 1 ? 16 : 8;
 constexpr int kTile = 16;         // tokens a warp takes at a time; divides every page size
 constexpr int kMaxWorkers = 2560;  // warps that take work, at most
 // What a warp spends on a (sequence, head) pair besides its tiles (the table, the queries, the
@@ -57,7 +59,7 @@ template <int D> constexpr int kStages = D == 64 ? 4 : 3;
 template <int D, int NT> constexpr int kResident = D == 64 ? (NT == 2 ? 3 : 4) : (D == 128 ? 3 : 2);
 template <int D> constexpr int kStageBytes = 2 * kTile * D;  // codes of K and V
 template <int D> constexpr int kRingBytes = kStages<D> * kStageBytes<D>;
-template <int D> constexpr int kSmemBytes = kWarps * kRingBytes<D> + 1024;  // the rings begin on a swizzle atom
+template <int D, int WARPS> constexpr int kSmemBytes = WARPS * kRingBytes<D> + 1024;  // the rings begin on a swizzle atom
 // tau: three bits for each of 8 rows, every fourth bit left out.  d = 64 has two tokens in a
 // 128-byte line, the others one (or half of one).
 template <int D> constexpr uint32_t kTau = D == 64 ? 0x65217430u : 0x37621540u;
@@ -97,6 +99,13 @@ __device__ __forceinline__ int seq_tiles(const Params &p, int b) { return (seq_l
 
 __device__ __forceinline__ float row_lse(float m, float l) {
     return l == 0.f ? neg_inf() : ((m == neg_inf() ? 0.f : m) + log2f(l)) * 0.693147180559945f;
+}
+
+__device__ __forceinline__ void store_out(const Params &p, long long at, float4 o) {
+    if (p.o_bf16)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    else
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) = o;
 }
 
 // The plan: all (sequence, key/value head) pairs with tiles, in that order, lie on a line,
@@ -204,36 +213,43 @@ __device__ __forceinline__ void v_operands(uint32_t (&a)[2][4], const VWords<D> 
 
 __device__ __forceinline__ bool has_nan_code(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// One warp: a run of the line, pair by pair.
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, kResident<D, NT>)
+// Split (WARPS = kWarps): one warp takes a run of the line, pair by pair.
+// Direct (kDirectWarps): a CTA takes one pair, its warps parts of the pair's tiles,
+// which are merged in shared memory: one launch and no partial results in memory, for
+// lengths at which that counts.
+template <int D, int NT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == kWarps ? kResident<D, NT> : 1)
 fa_cache_attn_kernel(const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t s_bar[kWarps][kStages<D>];
-    __shared__ int s_abort[kWarps];
+    __shared__ __align__(8) uint64_t s_bar[WARPS][kStages<D>];
+    __shared__ int s_abort[WARPS];
+    constexpr bool DIRECT = WARPS != kWarps;
     constexpr int KJ = D / 64;               // 16-byte runs of a key for each lane
     constexpr int T = kStep<D>, S = kStages<D>;
     constexpr int CH = T == 1 ? 2 : 1;       // sums that a tile's scores are split into
     static_assert(S % T == 0 && 32 % T == 0, "steps do not straddle the ring's end or a window's");
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!DIRECT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         prefetch_tensormap(&p.tm_k);
         prefetch_tensormap(&p.tm_v);
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    // neighbours on the line are on different SMs: few workers still use them all
-    const int id = warp * gridDim.x + blockIdx.x;
-    if (id >= p.chunks * p.workers) return;
+    // split: neighbours on the line are on different SMs, so that few workers still use them all
+    const int id = DIRECT ? blockIdx.x : warp * gridDim.x + blockIdx.x;
+    if (!DIRECT && id >= p.chunks * p.workers) return;
     const int chunk = id % p.chunks, worker = id / p.chunks;
     const int row0 = chunk * 8 * NT;
-    const Plan plan = make_plan<D>(p);
-    if ((long long)worker * plan.per >= plan.total) return;
-    int at = worker * plan.per;
-    const int end = at + min(plan.total - at, plan.per);
-    int b, first;
-    locate(p, plan, at, b, first);
+    int per = 0, at = 0, end = 0, b = 0, first = 0;
+    if constexpr (!DIRECT) {
+        const Plan plan = make_plan<D>(p);
+        per = plan.per;
+        if ((long long)worker * per >= plan.total) return;
+        at = worker * per;
+        end = at + min(plan.total - at, per);
+        locate(p, plan, at, b, first);
+    }
 
     const uint32_t ring = ((smem_u32(smem_raw) + 1023) & ~1023u) + warp * kRingBytes<D>;
     uint64_t *bar = s_bar[warp];
@@ -289,7 +305,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         if (lane == 0) {
             if (tile < 0) {
                 mbar_arrive(&bar[slot]);
-            } else if (p.drop_load <= 0 || i != p.drop_load - 1 || id != 0) {
+            } else if (p.drop_load <= 0 || i != p.drop_load - 1 || (id != 0 || (DIRECT && warp != 0))) {
                 const uint32_t dst = ring + slot * kStageBytes<D> + (keys ? 0 : kTile * D);
                 const CUtensorMap *map = keys ? &p.tm_k : &p.tm_v;
                 mbar_arrive_expect_tx(&bar[slot], kTile * D);
@@ -297,6 +313,19 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                 if constexpr (D == 256) tma_load_3d_at(dst + kTile * 128, map, &bar[slot], 128, 0, tile);
             }
         }
+    };
+    auto begin_pair = [&]() {
+        n_pad = (n_own + T - 1) / T * T;
+        q_row = ((long long)b * cv.H_kv + h) * p.rows + row0;
+        table = cv.table + b * cv.table_stride;
+        window(0);
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            if (i < n_pad) {
+                const int slot = slot0 + i < S ? slot0 + i : slot0 + i - S;
+                load(i, slot, true);
+                load(i, slot, false);
+            }
     };
     // Takes the next pair of the run and starts its copies; false at the run's end.
     auto next_pair = [&]() -> bool {
@@ -318,21 +347,22 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
             if (n_own > 0) break;  // else the run has none of the pair's tiles, only its begin
         }
         if (n_own <= 0) return false;
-        n_pad = (n_own + T - 1) / T * T;
-        q_row = ((long long)b * cv.H_kv + h) * p.rows + row0;
-        table = cv.table + b * cv.table_stride;
-        window(0);
-#pragma unroll
-        for (int i = 0; i < S; ++i)
-            if (i < n_pad) {
-                const int slot = slot0 + i < S ? slot0 + i : slot0 + i - S;
-                load(i, slot, true);
-                load(i, slot, false);
-            }
+        begin_pair();
         return true;
     };
 
-    bool more = next_pair();
+    bool more = true;
+    if constexpr (DIRECT) {
+        b = worker / cv.H_kv;
+        h = worker - b * cv.H_kv;
+        len = seq_len(p, b);
+        nb = (len + kTile - 1) / kTile;
+        t0 = (int)((long long)nb * warp / WARPS);
+        n_own = (int)((long long)nb * (warp + 1) / WARPS) - t0;
+        begin_pair();
+    } else {
+        more = next_pair();
+    }
     while (more) {
         // ---- queries: fp16 of each row times a power of two that brings its
         // largest magnitude to [2^14, 2^15); bf16's 8 bits stay exact but for
@@ -637,6 +667,59 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
             slot0 += T;
             if (slot0 == S) slot0 = 0, parity ^= 1;
         }
+        if constexpr (DIRECT) {
+            // ---- the warps' parts, normalised, in their rings, and their merge
+            constexpr int RS = D + 4;
+            static_assert(8 * NT * RS * 4 <= kRingBytes<D>, "the rows lie in the warp's ring");
+            __shared__ float2 s_ml[WARPS][8 * NT];
+            uint8_t *const base = smem_raw + (((smem_u32(smem_raw) + 1023) & ~1023u) - smem_u32(smem_raw));
+            float *rows = reinterpret_cast<float *>(base + warp * kRingBytes<D>);
+            __syncwarp();  // every lane has read its last tile
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float sum = l[t][k];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                    if (failed) sum = __int_as_float(0x7fffffff);
+                    const float f = sum == 0.f ? 0.f : ex2_approx(n[t][k] - m[t][k] - 7.f) / sum;
+                    const int r = 8 * t + 2 * c + k;
+                    if (g == 0) s_ml[warp][r] = make_float2(m[t][k], sum);
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) {
+                        const int d0 = D == 64 ? 8 * g + 4 * w : 128 * (w >> 2) + 16 * g + 4 * (w & 3);
+                        *reinterpret_cast<float4 *>(rows + r * RS + d0) =
+                            make_float4(acc[t][2 * w][k] * f, acc[t][2 * w][k + 2] * f, acc[t][2 * w + 1][k] * f,
+                                        acc[t][2 * w + 1][k + 2] * f);
+                    }
+                }
+            __syncthreads();
+            for (int k = threadIdx.x; k < 8 * NT * (D / 4); k += 32 * WARPS) {
+                const int r = k / (D / 4), d0 = 4 * (k % (D / 4));
+                if (row0 + r >= p.rows) break;
+                float top = neg_inf();
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_ml[w][r].x);
+                const float ref = top == neg_inf() ? 0.f : top;
+                float sum = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) {
+                    const float a = ex2_approx(s_ml[w][r].x - ref) * s_ml[w][r].y;
+                    const float4 y = *reinterpret_cast<const float4 *>(base + w * kRingBytes<D> + 4 * (r * RS + d0));
+                    sum += a;
+                    o.x += a * y.x, o.y += a * y.y, o.z += a * y.z, o.w += a * y.w;
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+                store_out(p, (q_row + r) * D + d0, o);
+                if (d0 == 0) p.lse[q_row + r] = row_lse(top, sum);
+            }
+            return;
+        }
+
         // ---- the next pair's copies start before this one's result is written
         const long long row = q_row;
         const bool whole = t0 == 0 && n_own == nb;
@@ -667,13 +750,10 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                     const int d0 = D == 64 ? 8 * g + 4 * w : 128 * (w >> 2) + 16 * g + 4 * (w & 3);
                     const float4 o = make_float4(acc[t][2 * w][k] * f, acc[t][2 * w][k + 2] * f,
                                                  acc[t][2 * w + 1][k] * f, acc[t][2 * w + 1][k + 2] * f);
-                    if (!whole)
-                        *reinterpret_cast<float4 *>(p.o_part + (part + r) * D + d0) = o;
-                    else if (p.o_bf16)
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + (row + r) * D + d0) =
-                            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+                    if (whole)
+                        store_out(p, (row + r) * D + d0, o);
                     else
-                        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + (row + r) * D + d0) = o;
+                        *reinterpret_cast<float4 *>(p.o_part + (part + r) * D + d0) = o;
                 }
             }
     }

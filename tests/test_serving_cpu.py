@@ -91,7 +91,7 @@ def test_rotary_null():
 
 # ---------------------------------------------------------------- refusals of the C ABI
 def _rotary(dim=64, **kw):
-    return fa.Rotary(dim, **kw)._ref
+    return ctypes.pointer(fa.Rotary(dim, **kw).struct)
 
 
 def _rope_status(**kw):
