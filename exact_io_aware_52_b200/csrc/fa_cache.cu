@@ -94,8 +94,8 @@ struct AttnPlan {
 // CTAs that one SM holds (the kernel's launch bounds).
 int attn_resident(int d, int nt) {
     namespace ca = fa::cattn;
-    if (d == 64) return nt == 1 ? ca::kResident<64, 1> : ca::kResident<64, 2>;
-    if (d == 128) return nt == 1 ? ca::kResident<128, 1> : ca::kResident<128, 2>;
+    if (d == 64) return nt < 2 ? ca::kResident<64, 1> : ca::kResident<64, 2>;
+    if (d == 128) return nt < 2 ? ca::kResident<128, 1> : ca::kResident<128, 2>;
     return ca::kResident<256, 1>;
 }
 
@@ -104,13 +104,14 @@ AttnPlan plan_attn(const fa_cache_attn_params *p, int resident) {
     AttnPlan a;
     const fa_cache &c = p->cache;
     a.rows = p->H / c.H_kv * p->N;
-    a.nt = (a.rows <= 8 || c.d == 256) ? 1 : 2;
-    a.chunks = (a.rows + 8 * a.nt - 1) / (8 * a.nt);
+    a.nt = a.rows <= 4 ? 0 : ((a.rows <= 8 || c.d == 256) ? 1 : 2);
+    const int per = ca::rows_of(a.nt);
+    a.chunks = (a.rows + per - 1) / per;
     long long w = resident / a.chunks;
     const long long tiles = (long long)c.B * c.H_kv * (((long long)c.max_pages * c.page) / ca::kTile);
     if (w > tiles) w = tiles;  // a worker takes one at least
     a.workers = w < 1 ? 1 : (int)w;
-    const size_t slots = (size_t)a.chunks * a.workers * 2 * 8 * a.nt;
+    const size_t slots = (size_t)a.chunks * a.workers * 2 * per;
     a.o_bytes = slots * c.d * sizeof(float);
     a.ml_bytes = slots * 2 * sizeof(float);
     return a;
@@ -124,7 +125,7 @@ bool attn_empty(const fa_cache_attn_params *p) {
 }
 
 template <int D, int WPR>
-fa_status launch_merge(const fa::cattn::Params &kp, int nt8, cudaStream_t s) {
+fa_status launch_merge(const fa::cattn::Params &kp, int rows_per, cudaStream_t s) {
     constexpr int warps = fa::cattn::kMergeWarps<WPR>, per_cta = warps / WPR;
     const long long rows = (long long)kp.c.B * kp.c.H_kv * kp.rows;
     cudaLaunchConfig_t cfg = {};
@@ -136,7 +137,7 @@ fa_status launch_merge(const fa::cattn::Params &kp, int nt8, cudaStream_t s) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa::cattn::fa_cache_merge_kernel<D, WPR>, kp, nt8) == cudaSuccess ? FA_OK
+    return cudaLaunchKernelEx(&cfg, fa::cattn::fa_cache_merge_kernel<D, WPR>, kp, rows_per) == cudaSuccess ? FA_OK
                                                                                                        : FA_ERR_CUDA;
 }
 
@@ -174,9 +175,18 @@ fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_
     // The merge is launched while the first kernel runs and waits in it for its results.  A pair
     // has about workers / pairs parts: one warp for a row, or more where there are many.
     const long long pairs = (long long)kp.c.B * kp.c.H_kv;
-    if (kp.workers <= 4 * pairs) return launch_merge<D, 1>(kp, 8 * NT, s);
-    if (kp.workers <= 64 * pairs) return launch_merge<D, 8>(kp, 8 * NT, s);
-    return launch_merge<D, 32>(kp, 8 * NT, s);
+    if (kp.workers <= 4 * pairs) return launch_merge<D, 1>(kp, ca::rows_of(NT), s);
+    if (kp.workers <= 64 * pairs) return launch_merge<D, 8>(kp, ca::rows_of(NT), s);
+    return launch_merge<D, 32>(kp, ca::rows_of(NT), s);
+}
+
+template <int D>
+fa_status launch_attn_d(const fa::cattn::Params &kp, int nt, int dev, int sms, cudaStream_t s) {
+    if (nt == 0) return launch_attn<D, 0>(kp, dev, sms, s);
+    if constexpr (D < 256) {
+        if (nt == 2) return launch_attn<D, 2>(kp, dev, sms, s);
+    }
+    return launch_attn<D, 1>(kp, dev, sms, s);
 }
 
 }  // namespace
@@ -330,11 +340,8 @@ fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream) {
         (st = fa_detail::encode_cache_map(&kp.tm_v, pages ? c.v : p->workspace, tiles, lines, line)) != FA_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    switch (c.d) {
-        case 64: return a.nt == 1 ? launch_attn<64, 1>(kp, dev, sms, s) : launch_attn<64, 2>(kp, dev, sms, s);
-        case 128: return a.nt == 1 ? launch_attn<128, 1>(kp, dev, sms, s) : launch_attn<128, 2>(kp, dev, sms, s);
-        default: return launch_attn<256, 1>(kp, dev, sms, s);
-    }
+    return c.d == 64 ? launch_attn_d<64>(kp, a.nt, dev, sms, s)
+                     : (c.d == 128 ? launch_attn_d<128>(kp, a.nt, dev, sms, s) : launch_attn_d<256>(kp, a.nt, dev, sms, s));
 }
 
 }  // extern "C"

@@ -12,11 +12,12 @@
 // 2^15, and 2^-24 the step of the smallest); O = acc * 2^(n - m - 7) / l.
 //
 // Tiles.  A warp takes 16 tokens of one key/value head at a time.  S^T = K Q^T and
-// O^T = V^T P^T are computed transposed (mma m16n8k16, tokens or components
+// O^T = V^T P^T are computed transposed (tokens or components
 // on the 16 side, query rows on the 8 side), so that the 4 to 8 query rows
 // that share a key fill the tensor core's narrow side and the codes are the
-// A operand.  tcgen05 would want 128 rows: at 8 rows 15/16 of it would be idle, and the
-// codes would have to go back to shared memory as fp16 for it.
+// A operand.  tcgen05 would want 128 rows: at 8 rows 15/16 of it would be idle.
+// Both run on fp16 (mma m16n8k16), to which the codes convert exactly.  (The E4M3 form of
+// mma, with the queries in two parts, took more instructions: 408 for each tile of d = 128 against 334.)
 // Every warp works by itself: it has a ring of tiles that TMA fills (one lane issues),
 // with an mbarrier for each, and no barrier is shared between warps.  Which token
 // or component a row of a matrix stands for is free; it is chosen such that a
@@ -42,7 +43,7 @@ namespace cattn {
 constexpr int kWarps = 4;         // of a CTA when the keys are split
 // Of a CTA that takes a whole pair: as many as its registers and rings allow, since one warp for
 // each scheduler takes 0.9 us for a tile, which more warps hide.
-template <int D, int NT> constexpr int kDirectWarps = D <= 128 && NT == 1 ? 16 : 8;
+template <int D, int NT> constexpr int kDirectWarps = D <= 128 && NT < 2 ? 16 : 8;
 constexpr int kTile = 16;         // tokens a warp takes at a time; divides every page size
 constexpr int kMaxWorkers = 2560;  // warps that take work, at most
 // What a warp spends on a (sequence, head) pair besides its tiles (the table, the queries, the
@@ -67,8 +68,8 @@ template <int D>
 __device__ __forceinline__ int tau(int r) { return (kTau<D> >> (4 * r)) & 7; }
 // Byte b of a tile of 128-byte lines under the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(uint32_t b) { return b ^ (((b >> 7) & 7) << 4); }
-// query rows one CTA handles: 8 NT
-template <int D> constexpr int kMaxNT = D == 256 ? 1 : 2;
+// Query rows that one warp handles: 8 NT, or 4 for NT = 0.
+__host__ __device__ constexpr int rows_of(int nt) { return nt ? 8 * nt : 4; }
 
 struct Params {
     CUtensorMap tm_k, tm_v;  // codes as [tiles][16 d / line][line], line = 128 bytes (256 for d = 256), swizzled
@@ -78,10 +79,10 @@ struct Params {
     float *lse;
     const int32_t *k_len;
     int32_t *status;
-    float *o_part;        // [chunk][worker][2][8 NT][D]
-    float2 *ml_part;      // [chunk][worker][2][8 NT] (m, l)
+    float *o_part;        // [chunk][worker][2][rows][D]
+    float2 *ml_part;      // [chunk][worker][2][rows] (m, l)
     int N, rows;          // query tokens; rows that share a key/value head: group * N
-    int chunks, workers;  // blocks of 8 NT rows; warps for each of them
+    int chunks, workers;  // blocks of rows; warps for each of them
     int causal, o_bf16;
     float scale_log2;
     uint64_t timeout_ns;
@@ -226,7 +227,11 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     constexpr bool DIRECT = WARPS != kWarps;
     constexpr int KJ = D / 64;               // 16-byte runs of a key for each lane
     constexpr int T = kStep<D>, S = kStages<D>;
+    // NT = 0: at most 4 rows, in the products' even columns: one for each lane of a group of 4, so that the
+    // softmax has no idle half.  Else 8 NT rows, two for each lane of a group and product.
     constexpr int CH = T == 1 ? 2 : 1;       // sums that a tile's scores are split into
+    constexpr bool PACK = NT == 0;
+    constexpr int G = PACK ? 1 : NT, RL = PACK ? 1 : 2, R = rows_of(NT);
     static_assert(S % T == 0 && 32 % T == 0, "steps do not straddle the ring's end or a window's");
 
     if (!DIRECT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -240,7 +245,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     const int id = DIRECT ? blockIdx.x : warp * gridDim.x + blockIdx.x;
     if (!DIRECT && id >= p.chunks * p.workers) return;
     const int chunk = id % p.chunks, worker = id / p.chunks;
-    const int row0 = chunk * 8 * NT;
+    const int row0 = chunk * R;
     int per = 0, at = 0, end = 0, b = 0, first = 0;
     if constexpr (!DIRECT) {
         const Plan plan = make_plan<D>(p);
@@ -364,16 +369,15 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         more = next_pair();
     }
     while (more) {
-        // ---- queries: fp16 of each row times a power of two that brings its
-        // largest magnitude to [2^14, 2^15); bf16's 8 bits stay exact but for
-        // components 2^-29 below the row's largest
-        uint32_t qf[NT][D / 16][2];
-        float rs[NT][2];   // of rows 2c and 2c + 1: scale * log2(e) / that power
-        int lim[NT][2];    // and their number of keys
+        // ---- queries: fp16 of each row times a power of two that brings its largest magnitude
+        // to [2^14, 2^15); bf16's 8 bits stay exact but for components 2^-28 below the row's largest
+        uint32_t qf[G][D / 16][2];
+        float rs[G][RL];   // of this lane's rows: scale * log2(e) / that power
+        int lim[G][RL];    // and their number of keys
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int r = 8 * t + g;
-            const bool live = row0 + r < p.rows;
+        for (int t = 0; t < G; ++t) {
+            const int r = PACK ? g >> 1 : 8 * t + g;
+            const bool live = row0 + r < p.rows && !(PACK && (g & 1));  // PACK: odd columns are zero
             const uint16_t *q = p.q + (q_row + r) * D + 16 * c;
             uint32_t raw[KJ][8];
             uint32_t mag = 0;
@@ -395,8 +399,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
             }
             mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
             mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-            // up = 2^(14 - E), E the exponent of the largest (2^126 at most: a row of subnormal
-            // values stays below 2^14)
+            // 2^126 at most: a row of subnormal values stays below 2^14
             const int e = min(max(14 - ((int)(mag >> 7) - 127), -126), 126);
             const float up = __uint_as_float((uint32_t)(e + 127) << 23);
 #pragma unroll
@@ -409,25 +412,24 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                         qf[t][4 * j + w][i] = pack_half2(bf16x2_lo(z) * up, bf16x2_hi(z) * up);
                     }
             const float f = __uint_as_float((uint32_t)(127 - e) << 23) * p.scale_log2;
-            rs[t][0] = __shfl_sync(0xffffffffu, f, 8 * c);
-            rs[t][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int row = row0 + 8 * t + 2 * c + i;
+            for (int i = 0; i < RL; ++i) {
+                rs[t][i] = __shfl_sync(0xffffffffu, f, 8 * c + 4 * i);
+                const int row = row0 + (PACK ? c : 8 * t + 2 * c + i);
                 lim[t][i] = p.causal ? len - p.N + row % p.N + 1 : len;
             }
         }
         const int all = p.causal ? len - p.N + 1 : len;  // keys that every row sees
 
-        float acc[NT][D / 16][4];
-        float m[NT][2], n[NT][2], l[NT][2];
-        float m0[NT][2], n0[NT][2];  // what is added to a score: -m, and 7 - n (0 and 7 while nothing is seen)
+        float acc[G][D / 16][4];
+        float m[G][RL], n[G][RL], l[G][RL];
+        float m0[G][RL], n0[G][RL];  // what is added to a score: -m, and 7 - n (0 and 7 while nothing is seen)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < G; ++t) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < RL; ++i) {
                 m[t][i] = n[t][i] = neg_inf();
                 l[t][i] = m0[t][i] = 0.f;
                 n0[t][i] = 7.f;
@@ -468,15 +470,15 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
             }
 
             // ---- S^T
-            float s[T][NT][CH][4];
+            float s[T][G][CH][4];
 #pragma unroll
             for (int u = 0; u < T; ++u)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < G; ++t)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int x = 0; x < CH; ++x) s[u][t][x][k] = 0.f;
+                        for (int y = 0; y < CH; ++y) s[u][t][y][k] = 0.f;
 #pragma unroll
             for (int j = 0; j < KJ; ++j) {
                 uint4 ka[T], kb[T];
@@ -497,7 +499,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                         half4(aw[w], a0, a2);
                         half4(bw[w], a1, a3);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
+                        for (int t = 0; t < G; ++t)
                             mma16816(s[u][t][w % CH], a0, a1, a2, a3, qf[t][4 * j + w][0], qf[t][4 * j + w][1]);
                     }
             }
@@ -510,39 +512,39 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                     load(i + u + S, slot0 + u, true);
                 }
 
-            // ---- scores in units of log2; x[..][0..1] token tau(g), x[..][2..3] token tau(g) + 8
-            float x[T][NT][4];
+            // ---- scores in units of log2 of this lane's rows: [i] of token tau(g), [RL + i] of tau(g) + 8
+            float x[T][G][2 * RL];
             bool raise = false;
 #pragma unroll
             for (int u = 0; u < T; ++u)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const float f[2] = {rs[t][0] * ks[u], rs[t][1] * ks[u]};
+                for (int t = 0; t < G; ++t) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float y = s[u][t][0][k];
-                        if constexpr (CH == 2) y += s[u][t][1][k];
-                        x[u][t][k] = y * f[k & 1];
+                    for (int k = 0; k < 2 * RL; ++k) {
+                        constexpr int step = PACK ? 2 : 1;  // PACK: the even columns
+                        float y = s[u][t][0][step * k];
+                        if constexpr (CH == 2) y += s[u][t][1][step * k];
+                        x[u][t][k] = y * (rs[t][k % RL] * ks[u]);
                     }
                     if (edge[u]) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (bad[u] || tok0[u] + tau<D>(g) + 8 * (k >> 1) >= lim[t][k & 1]) x[u][t][k] = neg_inf();
+                        for (int k = 0; k < 2 * RL; ++k)
+                            if (bad[u] || tok0[u] + tau<D>(g) + 8 * (k / RL) >= lim[t][k % RL]) x[u][t][k] = neg_inf();
                     }
                     // n - lv is +inf for a scale of 0 (and NaN, which fminf leaves out, if nothing is seen)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        raise |= fmaxf(x[u][t][k], x[u][t][k + 2]) > fminf(m[t][k], n[t][k] - lv[u]) + 8.f;
+                    for (int k = 0; k < RL; ++k)
+                        raise |= fmaxf(x[u][t][k], x[u][t][k + RL]) > fminf(m[t][k], n[t][k] - lv[u]) + 8.f;
                 }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < G; ++t)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < RL; ++k) {
                         float mn = m[t][k], nn = n[t][k];
 #pragma unroll
                         for (int u = 0; u < T; ++u) {
-                            float top = fmaxf(x[u][t][k], x[u][t][k + 2]);
+                            float top = fmaxf(x[u][t][k], x[u][t][k + RL]);
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -564,19 +566,20 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                         }
                     }
             }
-            uint32_t pb[T][NT][2];
+            uint32_t pb[T][G][2];
 #pragma unroll
             for (int u = 0; u < T; ++u)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float w[4];
+                for (int t = 0; t < G; ++t) {
+                    float w[2 * RL];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        l[t][k & 1] += ex2_approx(x[u][t][k] + m0[t][k & 1]);
-                        w[k] = ex2_approx(x[u][t][k] + (lv[u] + n0[t][k & 1]));
+                    for (int k = 0; k < 2 * RL; ++k) {
+                        l[t][k % RL] += ex2_approx(x[u][t][k] + m0[t][k % RL]);
+                        w[k] = ex2_approx(x[u][t][k] + (lv[u] + n0[t][k % RL]));
                     }
-                    pb[u][t][0] = transposed8x8(pack_half2(w[0], w[1]));
-                    pb[u][t][1] = transposed8x8(pack_half2(w[2], w[3]));
+                    // PACK: column 2 c has row c, column 2 c + 1 nothing
+                    pb[u][t][0] = transposed8x8(pack_half2(w[0], PACK ? 0.f : w[1]));
+                    pb[u][t][1] = transposed8x8(pack_half2(w[RL], PACK ? 0.f : w[2 * RL - 1]));
                 }
 
             // ---- O^T
@@ -637,14 +640,14 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                                 uint32_t a[2][4];
                                 v_operands<D>(a, vm, w);
 #pragma unroll
-                                for (int t = 0; t < NT; ++t)
+                                for (int t = 0; t < G; ++t)
 #pragma unroll
                                     for (int k = 0; k < 2; ++k) {
                                         float part[4] = {0.f, 0.f, 0.f, 0.f};
                                         mma16816(part, a[k][0], a[k][1], a[k][2], a[k][3], pb[u][t][0], pb[u][t][1]);
 #pragma unroll
                                         for (int j = 0; j < 4; ++j)
-                                            if ((row0 + 8 * t + 2 * c + (j & 1)) % p.N == tq) acc[t][2 * w + k][j] += part[j];
+                                            if ((row0 + (PACK ? c : 8 * t + 2 * c + (j & 1))) % p.N == tq) acc[t][2 * w + k][j] += part[j];
                                     }
                             }
                         }
@@ -654,7 +657,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                             uint32_t a[2][4];
                             v_operands<D>(a, v, w);
 #pragma unroll
-                            for (int t = 0; t < NT; ++t)
+                            for (int t = 0; t < G; ++t)
 #pragma unroll
                                 for (int k = 0; k < 2; ++k)
                                     mma16816(acc[t][2 * w + k], a[k][0], a[k][1], a[k][2], a[k][3], pb[u][t][0], pb[u][t][1]);
@@ -670,22 +673,22 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         if constexpr (DIRECT) {
             // ---- the warps' parts, normalised, in their rings, and their merge
             constexpr int RS = D + 4;
-            static_assert(8 * NT * RS * 4 <= kRingBytes<D>, "the rows lie in the warp's ring");
-            __shared__ float2 s_ml[WARPS][8 * NT];
+            static_assert(R * RS * 4 <= kRingBytes<D>, "the rows lie in the warp's ring");
+            __shared__ float2 s_ml[WARPS][R];
             uint8_t *const base = smem_raw + (((smem_u32(smem_raw) + 1023) & ~1023u) - smem_u32(smem_raw));
             float *rows = reinterpret_cast<float *>(base + warp * kRingBytes<D>);
             __syncwarp();  // every lane has read its last tile
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < G; ++t)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < RL; ++k) {
                     float sum = l[t][k];
                     sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                     if (failed) sum = __int_as_float(0x7fffffff);
                     const float f = sum == 0.f ? 0.f : ex2_approx(n[t][k] - m[t][k] - 7.f) / sum;
-                    const int r = 8 * t + 2 * c + k;
+                    const int r = PACK ? c : 8 * t + 2 * c + k;
                     if (g == 0) s_ml[warp][r] = make_float2(m[t][k], sum);
 #pragma unroll
                     for (int w = 0; w < D / 32; ++w) {
@@ -696,7 +699,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                     }
                 }
             __syncthreads();
-            for (int k = threadIdx.x; k < 8 * NT * (D / 4); k += 32 * WARPS) {
+            for (int k = threadIdx.x; k < R * (D / 4); k += 32 * WARPS) {
                 const int r = k / (D / 4), d0 = 4 * (k % (D / 4));
                 if (row0 + r >= p.rows) break;
                 float top = neg_inf();
@@ -723,20 +726,20 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         // ---- the next pair's copies start before this one's result is written
         const long long row = q_row;
         const bool whole = t0 == 0 && n_own == nb;
-        const long long part = ((((long long)chunk * p.workers + worker) * 2) + (t0 == 0 ? 1 : 0)) * 8 * NT;
+        const long long part = ((((long long)chunk * p.workers + worker) * 2) + (t0 == 0 ? 1 : 0)) * R;
         n_own = 0;
         more = !failed && next_pair();
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < G; ++t)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < RL; ++k) {
                 float sum = l[t][k];
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 if (failed) sum = __int_as_float(0x7fffffff);
                 const float f = sum == 0.f ? 0.f : ex2_approx(n[t][k] - m[t][k] - 7.f) / sum;
-                const int r = 8 * t + 2 * c + k;
+                const int r = PACK ? c : 8 * t + 2 * c + k;
                 if (row0 + r >= p.rows) continue;
                 if (g == 0) {
                     if (whole)
@@ -767,7 +770,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
 template <int WPR> constexpr int kMergeWarps = WPR < 4 ? 4 : WPR;
 
 template <int D, int WPR>
-__global__ void __launch_bounds__(32 * kMergeWarps<WPR>) fa_cache_merge_kernel(const __grid_constant__ Params p, int nt8) {
+__global__ void __launch_bounds__(32 * kMergeWarps<WPR>) fa_cache_merge_kernel(const __grid_constant__ Params p, int rows_per) {
     constexpr int W = D / 32, WARPS = kMergeWarps<WPR>;
     __shared__ float s_o[WPR > 1 ? WARPS : 1][WPR > 1 ? D : 1];
     __shared__ float2 s_ml[WARPS];
@@ -789,11 +792,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps<WPR>) fa_cache_merge_kernel(c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!inside || (nb && w0 == w1)) return;  // the one worker that had it has written it
     const int n = nb ? w1 - w0 + 1 : 0;
-    const int chunk = r / nt8;
+    const int chunk = r / rows_per;
     // part i is worker w0 + i's; the first begins the pair, the others continue it
     const long long base = ((long long)chunk * p.workers + w0) * 2;
-    const int rr = r - chunk * nt8;
-    auto index = [&](int i) { return (base + 2 * i + (i == 0 ? 1 : 0)) * nt8 + rr; };
+    const int rr = r - chunk * rows_per;
+    auto index = [&](int i) { return (base + 2 * i + (i == 0 ? 1 : 0)) * rows_per + rr; };
 
     float o[W];
 #pragma unroll

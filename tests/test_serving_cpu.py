@@ -231,10 +231,11 @@ def test_null_params():
 
 def test_attn_workspace_bytes():
     size = lambda cache=None, **kw: fb.load().fa_cache_attn_workspace_bytes(ctypes.byref(_attn_params(cache, **kw)))  # noqa: E731
-    # one pair of slots of 8 rows for each worker, 2560 workers at most
-    assert 0 < size() <= 2560 * 2 * 8 * (128 + 2) * 4
-    assert size(dict(B=1, H_kv=1, max_pages=1), H=1) == 4 * 2 * 8 * (128 + 2) * 4   # 4 tiles: no more workers
-    assert size(dict(B=64, max_pages=128)) == 2560 * 2 * 8 * (128 + 2) * 4
+    # one pair of slots of 4 or 8 rows for each worker, 2560 workers at most
+    assert 0 < size() <= 2560 * 2 * 4 * (128 + 2) * 4
+    assert size(dict(B=1, H_kv=1, max_pages=1), H=1) == 4 * 2 * 4 * (128 + 2) * 4   # 4 tiles: no more workers
+    assert size(dict(B=64, max_pages=128)) == 2560 * 2 * 4 * (128 + 2) * 4
+    assert size(dict(B=64, max_pages=128), H=16) == 2560 * 2 * 8 * (128 + 2) * 4
     assert size(H=64) >= size(H=8)
     assert size(H=0) == size(N=0) == size(H=3) == size(dict(page=5)) == size(dict(B=0)) == 0
     assert fb.status_string(fb.FA_ERR_BAD_PAGE) == "FA_ERR_BAD_PAGE"
