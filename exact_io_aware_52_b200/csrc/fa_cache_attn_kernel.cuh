@@ -259,7 +259,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     const uint32_t ring = ((smem_u32(smem_raw) + 1023) & ~1023u) + warp * kRingBytes<D>;
     uint64_t *bar = s_bar[warp];
     if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(&bar[i], 2);  // K and V of a tile
+        for (int i = 0; i < S; ++i) mbar_init(&bar[i], 1);
         fence_mbar_init();
         s_abort[warp] = 0;
     }
@@ -305,17 +305,18 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     // Copies of own tile i into the slot at `st`.  A page outside the pool, and the place of a
     // missing second tile of the last step, have nothing to copy: their phase
     // completes all the same.
-    auto load = [&](int i, int slot, bool keys) {
+    auto load = [&](int i, int slot) {
         const int tile = __shfl_sync(0xffffffffu, w_tile, i & 31);
         if (lane == 0) {
+            const uint32_t dst = ring + slot * kStageBytes<D>;
             if (tile < 0) {
                 mbar_arrive(&bar[slot]);
-            } else if (p.drop_load <= 0 || i != p.drop_load - 1 || (id != 0 || (DIRECT && warp != 0))) {
-                const uint32_t dst = ring + slot * kStageBytes<D> + (keys ? 0 : kTile * D);
-                const CUtensorMap *map = keys ? &p.tm_k : &p.tm_v;
-                mbar_arrive_expect_tx(&bar[slot], kTile * D);
-                tma_load_3d_at(dst, map, &bar[slot], 0, 0, tile);
-                if constexpr (D == 256) tma_load_3d_at(dst + kTile * 128, map, &bar[slot], 128, 0, tile);
+            } else if (p.drop_load <= 0 || i != p.drop_load - 1 || id != 0 || (DIRECT && warp != 0)) {
+                mbar_arrive_expect_tx(&bar[slot], kStageBytes<D>);
+                tma_load_3d_at(dst, &p.tm_k, &bar[slot], 0, 0, tile);
+                if constexpr (D == 256) tma_load_3d_at(dst + kTile * 128, &p.tm_k, &bar[slot], 128, 0, tile);
+                tma_load_3d_at(dst + kTile * D, &p.tm_v, &bar[slot], 0, 0, tile);
+                if constexpr (D == 256) tma_load_3d_at(dst + kTile * (D + 128), &p.tm_v, &bar[slot], 128, 0, tile);
             }
         }
     };
@@ -326,11 +327,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         window(0);
 #pragma unroll
         for (int i = 0; i < S; ++i)
-            if (i < n_pad) {
-                const int slot = slot0 + i < S ? slot0 + i : slot0 + i - S;
-                load(i, slot, true);
-                load(i, slot, false);
-            }
+            if (i < n_pad) load(i, slot0 + i < S ? slot0 + i : slot0 + i - S);
     };
     // Takes the next pair of the run and starts its copies; false at the run's end.
     auto next_pair = [&]() -> bool {
@@ -503,15 +500,6 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                             mma16816(s[u][t][w % CH], a0, a1, a2, a3, qf[t][4 * j + w][0], qf[t][4 * j + w][1]);
                     }
             }
-            // the keys' slots are free: every lane's reads were operands of the products above
-            __syncwarp();
-#pragma unroll
-            for (int u = 0; u < T; ++u)
-                if (i + u + S < n_pad) {
-                    if (((i + u + S) & 31) == 0) window(i + u + S);
-                    load(i + u + S, slot0 + u, true);
-                }
-
             // ---- scores in units of log2 of this lane's rows: [i] of token tau(g), [RL + i] of tau(g) + 8
             float x[T][G][2 * RL];
             bool raise = false;
@@ -664,8 +652,11 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                         }
                     }
                 }
-                __syncwarp();  // every lane has taken the values
-                if (i + u + S < n_pad) load(i + u + S, slot0 + u, false);
+                __syncwarp();  // every lane has taken its part of the tile
+                if (i + u + S < n_pad) {
+                    if (((i + u + S) & 31) == 0) window(i + u + S);
+                    load(i + u + S, slot0 + u);
+                }
             }
             slot0 += T;
             if (slot0 == S) slot0 = 0, parity ^= 1;
