@@ -57,7 +57,7 @@ template <int D> constexpr int kStep = D == 64 ? 2 : 1;
 template <int D> constexpr int kStages = D == 64 ? 4 : 3;
 // CTAs for each SM.  More tiles in flight are not better: d = 128 with one CTA more or a tile
 // more in the ring took 5 to 15 % longer.
-template <int D, int NT> constexpr int kResident = D == 64 ? (NT == 2 ? 3 : 4) : (D == 128 ? 3 : 2);
+template <int D, int NT> constexpr int kResident = D == 64 ? (NT == 2 ? 3 : 4) : (D == 128 && NT < 2 ? 3 : 2);
 template <int D> constexpr int kStageBytes = 2 * kTile * D;  // codes of K and V
 template <int D> constexpr int kRingBytes = kStages<D> * kStageBytes<D>;
 template <int D, int WARPS> constexpr int kSmemBytes = WARPS * kRingBytes<D> + 1024;  // the rings begin on a swizzle atom

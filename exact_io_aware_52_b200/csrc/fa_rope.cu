@@ -52,8 +52,8 @@ template <typename T> struct RawSlot;
 template <> struct RawSlot<uint16_t> {
     uint4 a, b;
     __device__ __forceinline__ void load(const uint16_t *x, const RotarySlot &at) {
-        a = __ldcs(reinterpret_cast<const uint4 *>(x + at.a));
-        b = __ldcs(reinterpret_cast<const uint4 *>(x + at.b));
+        a = *reinterpret_cast<const uint4 *>(x + at.a);
+        b = *reinterpret_cast<const uint4 *>(x + at.b);
     }
     __device__ __forceinline__ void get(float (&v)[16]) const {
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -64,10 +64,10 @@ template <> struct RawSlot<uint16_t> {
 template <> struct RawSlot<float> {
     float4 a[4];
     __device__ __forceinline__ void load(const float *x, const RotarySlot &at) {
-        a[0] = __ldcs(reinterpret_cast<const float4 *>(x + at.a));
-        a[1] = __ldcs(reinterpret_cast<const float4 *>(x + at.a) + 1);
-        a[2] = __ldcs(reinterpret_cast<const float4 *>(x + at.b));
-        a[3] = __ldcs(reinterpret_cast<const float4 *>(x + at.b) + 1);
+        a[0] = reinterpret_cast<const float4 *>(x + at.a)[0];
+        a[1] = reinterpret_cast<const float4 *>(x + at.a)[1];
+        a[2] = reinterpret_cast<const float4 *>(x + at.b)[0];
+        a[3] = reinterpret_cast<const float4 *>(x + at.b)[1];
     }
     __device__ __forceinline__ void get(float (&v)[16]) const {
 #pragma unroll
@@ -81,8 +81,11 @@ template <> struct RawSlot<float> {
 // all of them (they cost about as much as turning 4 heads); it has UN heads'
 // loads in flight.  The lanes of a warp lie along the components and then
 // along the tokens: whole 128-byte lines whichever way the strides run.
+// Measured: bf16 32 + 8 heads of 2 x 8192 tokens, d = 128, 58.5 us or 5.7 TB/s (64 registers;
+// 4 heads in flight with 80: 64 us; 16 or 20 heads a thread: 60); fp32 to bf16, 16 + 16 heads of 2 x 4097
+// tokens, half of d turned, 35.7 us or 5.6 TB/s (2 heads in flight: 38).
 template <typename TI, typename TO>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 4 : 2)
 fa_rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ uint64_t step[FA_ROTARY_MAX_DIM / 2];
     if (threadIdx.x < (p.dim >> 1)) step[threadIdx.x] = p.step[threadIdx.x];
@@ -100,7 +103,7 @@ fa_rope_kernel(const __grid_constant__ RopeParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) rotary_cs(step[rotary_pair(slot, j, p.dim, p.interleaved)], pos, p.amplitude, p.sign, c[j], s[j]);
     }
-    constexpr int UN = 2;
+    constexpr int UN = sizeof(TI) == 2 ? 2 : 4;
     const int h0 = blockIdx.y * p.chunk, h1 = min(h0 + p.chunk, p.heads);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
