@@ -83,6 +83,7 @@ struct Params {
     float2 *ml_part;      // [chunk][worker][2][rows] (m, l)
     int N, rows;          // query tokens; rows that share a key/value head: group * N
     int chunks, workers;  // blocks of rows; warps for each of them
+    int cluster;          // CTAs for each pair (direct)
     int causal, o_bf16;
     float scale_log2;
     uint64_t timeout_ns;
@@ -97,6 +98,22 @@ __device__ __forceinline__ int seq_len(const Params &p, int b) {
     return (int)min((long long)n, cap);
 }
 __device__ __forceinline__ int seq_tiles(const Params &p, int b) { return (seq_len(p, b) + kTile - 1) / kTile; }
+
+// All threads of a cluster's CTAs; what they wrote to shared memory before is visible to the others after.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Two floats of CTA `rank` of the cluster, at the place of this CTA's shared-memory address.
+__device__ __forceinline__ float2 peer_float2(uint32_t addr, int rank) {
+    float2 r;
+    asm volatile("{\n\t.reg .b32 a;\n\t"
+                 "mapa.shared::cluster.u32 a, %2, %3;\n\t"
+                 "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+                 : "=f"(r.x), "=f"(r.y)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return r;
+}
 
 __device__ __forceinline__ float row_lse(float m, float l) {
     return l == 0.f ? neg_inf() : ((m == neg_inf() ? 0.f : m) + log2f(l)) * 0.693147180559945f;
@@ -215,9 +232,9 @@ __device__ __forceinline__ void v_operands(uint32_t (&a)[2][4], const VWords<D> 
 __device__ __forceinline__ bool has_nan_code(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 // Split (WARPS = kWarps): one warp takes a run of the line, pair by pair.
-// Direct (kDirectWarps): a CTA takes one pair, its warps parts of the pair's tiles,
-// which are merged in shared memory: one launch and no partial results in memory, for
-// lengths at which that counts.
+// Direct (kDirectWarps): a cluster of CTAs takes one pair, its warps parts of the pair's
+// tiles, which are merged in shared memory, the CTA's first and then the cluster's: one launch and
+// no partial results in memory, for lengths at which that counts.
 template <int D, int NT, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == kWarps ? kResident<D, NT> : 1)
 fa_cache_attn_kernel(const __grid_constant__ Params p) {
@@ -242,7 +259,8 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     // split: neighbours on the line are on different SMs, so that few workers still use them all
-    const int id = DIRECT ? blockIdx.x : warp * gridDim.x + blockIdx.x;
+    const int rank = DIRECT ? blockIdx.x % p.cluster : 0;  // of a cluster's CTAs
+    const int id = DIRECT ? blockIdx.x / p.cluster : warp * gridDim.x + blockIdx.x;
     if (!DIRECT && id >= p.chunks * p.workers) return;
     const int chunk = id % p.chunks, worker = id / p.chunks;
     const int row0 = chunk * R;
@@ -311,7 +329,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
             const uint32_t dst = ring + slot * kStageBytes<D>;
             if (tile < 0) {
                 mbar_arrive(&bar[slot]);
-            } else if (p.drop_load <= 0 || i != p.drop_load - 1 || id != 0 || (DIRECT && warp != 0)) {
+            } else if (p.drop_load <= 0 || i != p.drop_load - 1 || id != 0 || (DIRECT && warp + rank != 0)) {
                 mbar_arrive_expect_tx(&bar[slot], kStageBytes<D>);
                 tma_load_3d_at(dst, &p.tm_k, &bar[slot], 0, 0, tile);
                 if constexpr (D == 256) tma_load_3d_at(dst + kTile * 128, &p.tm_k, &bar[slot], 128, 0, tile);
@@ -359,8 +377,9 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         h = worker - b * cv.H_kv;
         len = seq_len(p, b);
         nb = (len + kTile - 1) / kTile;
-        t0 = (int)((long long)nb * warp / WARPS);
-        n_own = (int)((long long)nb * (warp + 1) / WARPS) - t0;
+        const int part = rank * WARPS + warp, parts = p.cluster * WARPS;
+        t0 = (int)((long long)nb * part / parts);
+        n_own = (int)((long long)nb * (part + 1) / parts) - t0;
         begin_pair();
     } else {
         more = next_pair();
@@ -665,7 +684,8 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
             // ---- the warps' parts, normalised, in their rings, and their merge
             constexpr int RS = D + 4;
             static_assert(R * RS * 4 <= kRingBytes<D>, "the rows lie in the warp's ring");
-            __shared__ float2 s_ml[WARPS][R];
+            __shared__ float2 s_ml[WARPS][R], s_row[R];
+            __shared__ __align__(16) float s_o[R][D];
             uint8_t *const base = smem_raw + (((smem_u32(smem_raw) + 1023) & ~1023u) - smem_u32(smem_raw));
             float *rows = reinterpret_cast<float *>(base + warp * kRingBytes<D>);
             __syncwarp();  // every lane has read its last tile
@@ -708,9 +728,39 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                 }
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+                if (p.cluster == 1) {
+                    store_out(p, (q_row + r) * D + d0, o);
+                    if (d0 == 0) p.lse[q_row + r] = row_lse(top, sum);
+                } else {
+                    *reinterpret_cast<float4 *>(&s_o[r][d0]) = o;
+                    if (d0 == 0) s_row[r] = make_float2(top, sum);
+                }
+            }
+            if (p.cluster == 1) return;
+            // ---- the CTAs' parts: each CTA merges its share of the components
+            cluster_sync();
+            for (int k = threadIdx.x * p.cluster + rank; k < R * (D / 4); k += 32 * WARPS * p.cluster) {
+                const int r = k / (D / 4), d0 = 4 * (k % (D / 4));
+                if (row0 + r >= p.rows) break;
+                const uint32_t row_at = smem_u32(&s_row[r]), o_at = smem_u32(&s_o[r][d0]);
+                float top = neg_inf();
+                for (int i = 0; i < p.cluster; ++i) top = fmaxf(top, peer_float2(row_at, i).x);
+                const float ref = top == neg_inf() ? 0.f : top;
+                float sum = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = 0; i < p.cluster; ++i) {
+                    const float2 ml = peer_float2(row_at, i);
+                    const float a = ex2_approx(ml.x - ref) * ml.y;
+                    const float2 y = peer_float2(o_at, i), z = peer_float2(o_at + 8, i);
+                    sum += a;
+                    o.x += a * y.x, o.y += a * y.y, o.z += a * z.x, o.w += a * z.y;
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
                 store_out(p, (q_row + r) * D + d0, o);
                 if (d0 == 0) p.lse[q_row + r] = row_lse(top, sum);
             }
+            cluster_sync();  // no CTA ends while another reads its part
             return;
         }
 

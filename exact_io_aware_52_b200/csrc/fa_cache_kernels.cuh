@@ -100,6 +100,22 @@ __device__ __forceinline__ float key_component(const AppendParams &p, const uint
     return first ? a : b;
 }
 
+// The scale of a page whose new values reach amax (bits), and its inverse; `held`: the page holds tokens
+// from before, with the scale `before`.
+struct ScaleUpdate {
+    float now, inv;
+    bool grows;  // the page's earlier codes have to follow
+};
+__device__ __forceinline__ ScaleUpdate update_scale(bool held, float before, uint32_t amax) {
+    const float mine = page_scale(__uint_as_float(amax));
+    ScaleUpdate r;
+    r.now = held ? fmaxf(before, mine) : mine;
+    r.grows = held && r.now != before;
+    // a power of two from 2^-100 on, whose inverse is exact; the caller's own scale may be anything
+    r.inv = r.now == mine ? __uint_as_float(0x7f000000u - __float_as_uint(mine)) : 1.f / r.now;
+    return r;
+}
+
 // Where a block's (or warp's) new tokens lie: slots [s0, s1) of one page, the first of them
 // the sequence's new token t0.
 struct Touched {
@@ -166,7 +182,7 @@ __device__ __forceinline__ uint32_t key_amax(const float (&v)[16]) {
 __device__ __forceinline__ uint32_t value_amax(const Raw16 &x) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, x.w[j] & 0x7fff7fffu);
+    for (int j = 0; j < 8; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(x.w[j] & 0x7fff7fffu));
     return max(m << 16, m & 0xffff0000u);
 }
 // Of the finite ones.
@@ -235,22 +251,29 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
     const int per_row = c.d >> 4, row_log2 = 31 - __clz(per_row);
     const int turned = dim >> 4;  // slots of a token that are turned
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const uint16_t *xk = p.x[0] + b * p.xs[0][0] + (pg.t0 - pg.s0) * p.xs[0][2] + h0 * p.xs[0][1];
-    const uint16_t *xv = p.x[1] + b * p.xs[1][0] + (pg.t0 - pg.s0) * p.xs[1][2] + h0 * p.xs[1][1];
+    // This thread's first slot: token t, and where it lies in the inputs and in the page; its i-th one is
+    // `dt` tokens further on.  All of them advance by a head at a time.
+    const int t = threadIdx.x >> row_log2, dt = blockDim.x >> row_log2, slot = threadIdx.x & (per_row - 1);
+    const RotarySlot at = VEC ? rotary_slot(slot, c.d, dim) : plain_slot(slot);
+    const bool turns = slot < turned;
+    const uint16_t *xk = p.x[0] + b * p.xs[0][0] + h0 * p.xs[0][1] + (pg.t0 - pg.s0 + t) * p.xs[0][2];
+    const uint16_t *xv = p.x[1] + b * p.xs[1][0] + h0 * p.xs[1][1] + (pg.t0 - pg.s0 + t) * p.xs[1][2] + 16 * slot;
+    const long long unit0 = (long long)pg.page_id * c.H_kv + h0;
+    uint8_t *ck = c.k + (unit0 * c.page + t) * c.d, *cvv = c.v + (unit0 * c.page + t) * c.d + 16 * slot;
+    float *sk = c.k_scale + unit0, *sv = c.v_scale + unit0;
 
     Raw16 rk[SPT], rv[SPT];
     // This thread's slots of the head at xk, xv.
     auto load = [&]() {
 #pragma unroll
         for (int i = 0; i < SPT; ++i) {
-            const int kk = threadIdx.x + i * blockDim.x;
-            const int t = kk >> row_log2, slot = kk & (per_row - 1);
-            if (t < pg.s0 || t >= pg.s1) continue;
+            const int ti = t + i * dt;
+            if (ti < pg.s0 || ti >= pg.s1) continue;
             if constexpr (VEC) {
-                rk[i].load(xk + t * p.xs[0][2], rotary_slot(slot, c.d, dim));
-                rv[i].load(xv + t * p.xs[1][2], plain_slot(slot));
+                rk[i].load(xk + i * dt * p.xs[0][2], at);
+                rv[i].load(xv + i * dt * p.xs[1][2], RotarySlot{0, 8, false});
             } else {
-                rv[i].load_elements(xv + t * p.xs[1][2] + 16 * slot);
+                rv[i].load_elements(xv + i * dt * p.xs[1][2]);
             }
         }
     };
@@ -262,17 +285,18 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
             __syncthreads();
             const unsigned n = (pg.s1 - pg.s0) * 4 * turned;
             for (unsigned k = threadIdx.x; k < n; k += blockDim.x) {
-                const unsigned q = k / (unsigned)turned, slot = k - q * turned;
-                const int t = pg.s0 + (q >> 2), j = 2 * (q & 3);
+                const unsigned q = k / (unsigned)turned, e = k - q * turned;
+                const int tok = pg.s0 + (q >> 2), j = 2 * (q & 3);
                 float4 x;
-                rotary_cs(step[rotary_pair(slot, j, dim, p.interleaved)], (int)(pg.lo + t), p.amplitude, 1.f, x.x, x.y);
-                rotary_cs(step[rotary_pair(slot, j + 1, dim, p.interleaved)], (int)(pg.lo + t), p.amplitude, 1.f, x.z, x.w);
-                s_cs[(t * 4 + (q & 3)) * turned + slot] = x;
+                rotary_cs(step[rotary_pair(e, j, dim, p.interleaved)], (int)(pg.lo + tok), p.amplitude, 1.f, x.x, x.y);
+                rotary_cs(step[rotary_pair(e, j + 1, dim, p.interleaved)], (int)(pg.lo + tok), p.amplitude, 1.f, x.z, x.w);
+                s_cs[(tok * 4 + (q & 3)) * turned + e] = x;
             }
             __syncthreads();
         }
     }
 
+    const float4 *my_cs = s_cs + t * 4 * turned + slot;
     for (int h = h0; h < h1; ++h) {
         if (!AHEAD && h > h0) load();
         float k[SPT][16];
@@ -280,24 +304,23 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
         uint32_t mk = 0, mv = 0;
 #pragma unroll
         for (int i = 0; i < SPT; ++i) {
-            const int kk = threadIdx.x + i * blockDim.x;
-            const int t = kk >> row_log2, slot = kk & (per_row - 1);
-            if (t < pg.s0 || t >= pg.s1) continue;
+            const int ti = t + i * dt;
+            if (ti < pg.s0 || ti >= pg.s1) continue;
             v[i] = rv[i];
             if constexpr (VEC) {
                 rk[i].get(k[i]);
-                if (slot < turned) {
+                if (turns) {
                     float cs[8], sn[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 x = s_cs[(t * 4 + j) * turned + slot];
+                        const float4 x = my_cs[(i * dt * 4 + j) * turned];
                         cs[2 * j] = x.x, sn[2 * j] = x.y, cs[2 * j + 1] = x.z, sn[2 * j + 1] = x.w;
                     }
                     rotary_turn_slot(k[i], cs, sn, p.interleaved);
                 }
             } else {
                 for (int j = 0; j < 16; ++j)
-                    k[i][j] = key_component(p, xk + t * p.xs[0][2], 16 * slot + j, (int)(pg.lo + t));
+                    k[i][j] = key_component(p, xk + i * dt * p.xs[0][2], 16 * slot + j, (int)(pg.lo + ti));
             }
             mk = max(mk, key_amax(k[i]));
             mv = max(mv, value_amax(v[i]));
@@ -315,17 +338,16 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
             mk = __reduce_max_sync(0xffffffffu, x.x);
             mv = __reduce_max_sync(0xffffffffu, x.y);
         };
-        const long long unit = (long long)pg.page_id * c.H_kv + h;
         // read by all before thread 0 writes them
-        const float before_k = pg.s0 > 0 ? c.k_scale[unit] : 0.f, before_v = pg.s0 > 0 ? c.v_scale[unit] : 0.f;
+        const float before_k = pg.s0 > 0 ? *sk : 0.f, before_v = pg.s0 > 0 ? *sv : 0.f;
         block_max();
         const bool special_k = mk >= kInfBits, special_v = mv >= kInfBits;
         if (special_k || special_v) {  // rare; the same for the whole block
             mk = mv = 0;
 #pragma unroll
             for (int i = 0; i < SPT; ++i) {
-                const int t = (threadIdx.x + i * blockDim.x) >> row_log2;
-                if (t < pg.s0 || t >= pg.s1) continue;
+                const int ti = t + i * dt;
+                if (ti < pg.s0 || ti >= pg.s1) continue;
                 float y[16];
                 v[i].get(y);
                 mk = max(mk, amax_finite(k[i]));
@@ -334,30 +356,29 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
             __syncthreads();
             block_max();
         }
-        const float now_k = fmaxf(before_k, page_scale(__uint_as_float(mk)));
-        const float now_v = fmaxf(before_v, page_scale(__uint_as_float(mv)));
-        const float inv_k = 1.f / now_k, inv_v = 1.f / now_v;
-        const bool grows_k = pg.s0 > 0 && now_k != before_k, grows_v = pg.s0 > 0 && now_v != before_v;
-        uint8_t *ck = c.k + unit * c.page * c.d, *cvv = c.v + unit * c.page * c.d;
+        const ScaleUpdate uk = update_scale(pg.s0 > 0, before_k, mk), uv = update_scale(pg.s0 > 0, before_v, mv);
 #pragma unroll
         for (int i = 0; i < SPT; ++i) {
-            const int kk = threadIdx.x + i * blockDim.x;
-            const int t = kk >> row_log2, slot = kk & (per_row - 1);
-            if (t >= pg.s1) continue;
-            if (t >= pg.s0) {
+            const int ti = t + i * dt;
+            if (ti >= pg.s1) continue;
+            if (ti >= pg.s0) {
                 float y[16];
                 v[i].get(y);
-                store_slot(ck + t * c.d, VEC ? rotary_slot(slot, c.d, dim) : plain_slot(slot), k[i], inv_k, special_k);
-                store_slot(cvv + t * c.d, plain_slot(slot), y, inv_v, special_v);
+                store_slot(ck + i * dt * c.d, at, k[i], uk.inv, special_k);
+                store_slot(cvv + i * dt * c.d, RotarySlot{0, 8, false}, y, uv.inv, special_v);
             } else {  // exact ratios for powers of two
-                if (grows_k) rescale_run(ck + t * c.d + 16 * slot, before_k * inv_k);
-                if (grows_v) rescale_run(cvv + t * c.d + 16 * slot, before_v * inv_v);
+                if (uk.grows) rescale_run(ck + i * dt * c.d + 16 * slot, before_k * uk.inv);
+                if (uv.grows) rescale_run(cvv + i * dt * c.d, before_v * uv.inv);
             }
         }
         if (threadIdx.x == 0) {
-            if (pg.s0 == 0 || grows_k) c.k_scale[unit] = now_k;
-            if (pg.s0 == 0 || grows_v) c.v_scale[unit] = now_v;
+            if (pg.s0 == 0 || uk.grows) *sk = uk.now;
+            if (pg.s0 == 0 || uv.grows) *sv = uv.now;
         }
+        ck += c.page * c.d;
+        cvv += c.page * c.d;
+        ++sk;
+        ++sv;
     }
 }
 
@@ -409,22 +430,19 @@ __global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(con
             mk = __reduce_max_sync(0xffffffffu, here ? amax_finite(k) : 0u);
             mv = __reduce_max_sync(0xffffffffu, here ? amax_finite(v) : 0u);
         }
-        const float now_k = fmaxf(before_k, page_scale(__uint_as_float(mk)));
-        const float now_v = fmaxf(before_v, page_scale(__uint_as_float(mv)));
-        const float inv_k = 1.f / now_k, inv_v = 1.f / now_v;
+        const ScaleUpdate uk = update_scale(pg.s0 > 0, before_k, mk), uv = update_scale(pg.s0 > 0, before_v, mv);
         uint8_t *ck = c.k + unit * c.page * c.d, *cvv = c.v + unit * c.page * c.d;
         if (here) {
-            store_slot(ck + t * c.d, at, k, inv_k, special_k);
-            store_slot(cvv + t * c.d, plain_slot(slot), v, inv_v, special_v);
+            store_slot(ck + t * c.d, at, k, uk.inv, special_k);
+            store_slot(cvv + t * c.d, plain_slot(slot), v, uv.inv, special_v);
         }
-        const bool grows_k = pg.s0 > 0 && now_k != before_k, grows_v = pg.s0 > 0 && now_v != before_v;
-        if (grows_k)
-            for (int r = lane; r < pg.s0 * per_row; r += 32) rescale_run(ck + 16 * r, before_k * inv_k);
-        if (grows_v)
-            for (int r = lane; r < pg.s0 * per_row; r += 32) rescale_run(cvv + 16 * r, before_v * inv_v);
+        if (uk.grows)
+            for (int r = lane; r < pg.s0 * per_row; r += 32) rescale_run(ck + 16 * r, before_k * uk.inv);
+        if (uv.grows)
+            for (int r = lane; r < pg.s0 * per_row; r += 32) rescale_run(cvv + 16 * r, before_v * uv.inv);
         if (lane == 0) {
-            if (pg.s0 == 0 || grows_k) c.k_scale[unit] = now_k;
-            if (pg.s0 == 0 || grows_v) c.v_scale[unit] = now_v;
+            if (pg.s0 == 0 || uk.grows) c.k_scale[unit] = uk.now;
+            if (pg.s0 == 0 || uv.grows) c.v_scale[unit] = uv.now;
         }
     }
 }

@@ -288,6 +288,20 @@ def test_append_infinities_nan_zeros_and_extremes():
         assert torch.isnan(got).sum() == 3 and ws.min() == 2.0 ** -100
 
 
+def test_append_behind_a_scale_of_zero():
+    """A page whose scale is 0 holds zeros whatever its codes are, also when it gets a scale."""
+    H_kv, d, page = 1, 64, 16
+    for N in (1, 12):  # the kernel for few tokens and the other
+        kc, vc = (torch.full((1, H_kv, page, d), 0x38, dtype=torch.uint8, device=dev()) for _ in range(2))
+        ks, vs = (torch.zeros(1, H_kv, device=dev()) for _ in range(2))
+        x = torch.ones(1, H_kv, N, d, dtype=BF16, device=dev())
+        c = fa.PagedCache(kc, vc, ks, vs, ints([[0]]))
+        fa.cache_append(c, x, x, ints([3]))
+        k, v = fa.cache_gather(c, ints([3 + N]), 3 + N)
+        for t in (k, v):
+            assert (t[:, :, :3] == 0).all() and (t[:, :, 3:] == 1).all()
+
+
 def test_append_token_by_token_matches_a_prompt_scale():
     """Tokens one by one: the page's scale ends as the prompt's, the codes within the roundings on the way."""
     g = torch.Generator().manual_seed(20)
@@ -423,6 +437,19 @@ def test_attention(shape, out_dtype, causal):
     check_attention(o, lse, q, pool, lens, causal, d ** -0.5, page)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,N", [(4, 1), (8, 1), (6, 3)])
+@pytest.mark.parametrize("cap", [1, 100, 1000, 3000, 7000])
+def test_attention_clusters(d, H, N, cap):
+    """One to eight CTAs for a pair, by what the table can hold; most of it empty, or full."""
+    lens = [cap, 1, 0, cap // 2]
+    g = torch.Generator().manual_seed(d + cap)
+    pool = ref.pool(cap, lens, 1, 16, d)
+    q = torch.randn(4, H, N, d, generator=g).to(BF16)
+    o, lse = run_attention(q, pool, lens, True, d ** -0.5)
+    check_attention(o, lse, q, pool, lens, True, d ** -0.5, 16)
+
+
 @pytest.mark.parametrize("lens", [[70_001], [40_000, 3, 25_000], [129] * 67])
 def test_attention_many_parts(lens):
     g = torch.Generator().manual_seed(30)
@@ -546,6 +573,11 @@ def test_attention_wait_that_runs_out(d, drop):
     n = ints([2000 * 200])
     fa.cache_attention(long, q.to(dev()), n, True, 0.1, dev_status=status, timeout_ms=20, test_drop_load=drop)
     assert fa.read_device_status(status) == fb.FA_ERR_DEVICE_TIMEOUT
+    if drop == 1:  # and with clusters
+        status.zero_()
+        o, _ = fa.cache_attention(c, q.to(dev()), ints(lens), True, 0.1, dev_status=status, timeout_ms=20, test_drop_load=drop)
+        assert fa.read_device_status(status) == fb.FA_ERR_DEVICE_TIMEOUT
+        assert torch.isnan(o).all()
     o, lse = run_attention(q, pool, lens, True, 0.1, cache=c)
     check_attention(o, lse, q, pool, lens, True, 0.1, 16)
 
