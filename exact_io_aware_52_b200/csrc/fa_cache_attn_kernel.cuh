@@ -378,8 +378,8 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         len = seq_len(p, b);
         nb = (len + kTile - 1) / kTile;
         const int part = rank * WARPS + warp, parts = p.cluster * WARPS;
-        t0 = (int)((long long)nb * part / parts);
-        n_own = (int)((long long)nb * (part + 1) / parts) - t0;
+        t0 = (nb * part + parts - 1) / parts;  // a few tiles for each of up to 128 warps: no overflow
+        n_own = (nb * (part + 1) + parts - 1) / parts - t0;
         begin_pair();
     } else {
         more = next_pair();
