@@ -21,8 +21,29 @@ _SCALINGS = {"none": fb.FA_ROTARY_NONE, "linear": fb.FA_ROTARY_LINEAR, "base": f
              "parts": fb.FA_ROTARY_PARTS}
 _DTYPES = {torch.bfloat16: fb.FA_T_BF16, torch.float32: fb.FA_T_F32}
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream
+
+
+def _internal(path, default):
+    """A function of torch's internals that does a fraction of the public one's work on the host, if this
+    torch has it."""
+    at = torch._C
+    for name in path.split("."):
+        at = getattr(at, name, None)
+        if at is None:
+            return default
+    return at
+
+
+_raw_stream = _internal("_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = _internal("_cuda_getDevice", torch.cuda.current_device)
+# (size, strides, dtype), on the current device
+_empty_strided = _internal("_dynamo.guards._empty_strided_cuda",
+                           lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda"))
+
+
+def _empty(B, H, N, d, dtype):
+    return _empty_strided((B, H, N, d), (H * N * d, N * d, d, 1), dtype)
+
 
 # A decoding step makes several of these calls for kernels of a few microseconds, so the parameter
 # structures are packed in one go (filling a ctypes.Structure takes several times as long).
@@ -80,9 +101,9 @@ def _heads(t, name, dev):
 
 def _elsewhere(dev, stream):
     """The given device and stream as the current ones, so that tensors allocated
-    meanwhile belong to that stream; None if they are that already."""
+    meanwhile belong to that stream."""
     if stream is None:
-        return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+        return torch.cuda.device(dev)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
@@ -169,15 +190,12 @@ def rope(rotary, q, k=None, *, pos=None, pos0=0, inverse=False, out_dtype=None, 
             _refuse("pos must be int32 [B, N] or [N] on the same device, contiguous along the tokens")
         pos_at = pos.data_ptr()
         pos_stride = pos.stride(0) if len(sp) == 2 else 0
-    there = _elsewhere(dev, stream)
-    if there is not None:
-        with there:
+    if stream is not None or dev != _current_device():
+        with _elsewhere(dev, stream):
             return rope(rotary, q, k, pos=pos, pos0=pos0, inverse=inverse, out_dtype=out_dtype, out=out)
 
-    c1, c2 = N * d, H * N * d
     if yq is None:
-        # like q, its strides too, where those are the contiguous ones
-        yq = torch.empty_like(q) if sq == (c2, c1, d, 1) and y_dtype is q.dtype else q.new_empty((B, H, N, d), dtype=y_dtype)
+        yq = _empty(B, H, N, d, y_dtype)
     syq = yq.stride()
     if k is None:
         p = _pack(_ROPE, q.data_ptr(), yq.data_ptr(), H, sq[0], sq[1], sq[2], syq[0], syq[1], syq[2],
@@ -185,8 +203,7 @@ def rope(rotary, q, k=None, *, pos=None, pos0=0, inverse=False, out_dtype=None, 
                        B, N, d, x_type, y_type, pos_at, pos_stride, pos0, 1 if inverse else 0, rotary._address)
     else:
         if yk is None:
-            yk = torch.empty_like(k) if sk == (Hk * c1, c1, d, 1) and y_dtype is q.dtype else \
-                k.new_empty((B, Hk, N, d), dtype=y_dtype)
+            yk = _empty(B, Hk, N, d, y_dtype)
         syk = yk.stride()
         p = _pack(_ROPE, q.data_ptr(), yq.data_ptr(), H, sq[0], sq[1], sq[2], syq[0], syq[1], syq[2],
                        k.data_ptr(), yk.data_ptr(), Hk, sk[0], sk[1], sk[2], syk[0], syk[1], syk[2],
@@ -255,11 +272,10 @@ def cache_append(cache, k, v, start, *, n_new=None, rotary=None, dev_status=None
         _APPEND, k.data_ptr(), v.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], N,
         _ints(start, "start", B, dev), _ints(n_new, "n_new", B, dev), 0 if rotary is None else rotary._address,
         _ints(dev_status, "dev_status", 1, dev))
-    there = _elsewhere(dev, stream)
-    if there is None:
+    if stream is None and dev == _current_device():
         st = _call("fa_cache_append")(p, _raw_stream(dev))
     else:
-        with there:
+        with _elsewhere(dev, stream):
             st = _call("fa_cache_append")(p, _raw_stream(dev))
     if st:
         raise fb.FaError(st, "fa_cache_append")
@@ -280,13 +296,11 @@ def cache_gather(cache, k_len, N_k, *, out=None, dev_status=None, stream=None):
                 _refuse(f"out must be two contiguous bf16 tensors of shape {shape}")
     if k_len is None:
         _refuse("k_len must be given")
-    there = _elsewhere(dev, stream)
-    if there is not None:
-        with there:
+    if stream is not None or dev != _current_device():
+        with _elsewhere(dev, stream):
             return cache_gather(cache, k_len, N_k, out=out, dev_status=dev_status)
     if out is None:
-        ref = cache.k_scale
-        out = (ref.new_empty(shape, dtype=_BF16), ref.new_empty(shape, dtype=_BF16))
+        out = (_empty(*shape, _BF16), _empty(*shape, _BF16))
     k, v = out
     p = cache._packed + _pack(_GATHER, _ints(k_len, "k_len", cache.B, dev), k.data_ptr(), v.data_ptr(), N_k,
                                      _ints(dev_status, "dev_status", 1, dev))
@@ -342,22 +356,25 @@ def cache_attention(cache, q, k_len, causal, scale, *, out_dtype=None, out=None,
         _refuse("workspace must be contiguous and on the same device")
     if k_len is None:
         _refuse("k_len must be given")
-    there = _elsewhere(dev, stream)
-    if there is not None:
-        with there:
+    if stream is not None or dev != _current_device():
+        with _elsewhere(dev, stream):
             return cache_attention(cache, q, k_len, causal, scale, out_dtype=out_dtype, out=out, workspace=workspace,
                                    dev_status=dev_status, timeout_ms=timeout_ms, test_drop_load=test_drop_load)
     if out is None:
-        o = torch.empty_like(q) if o_dtype is _BF16 else q.new_empty(q.shape, dtype=_F32)
-        lse = q.new_empty((B, H, N), dtype=_F32)
+        o = _empty(B, H, N, d, o_dtype)
+        lse = _empty_strided((B, H, N), (H * N, N, 1), _F32)
+    scratch = 0
     if workspace is None:
         size = cache_attention_workspace_bytes(cache, H, N)
-        workspace = q.new_empty(size, dtype=torch.uint8)
+        if size:
+            workspace = _empty_strided((size,), (1,), torch.uint8)
+            scratch = workspace.data_ptr()
     else:
         size = workspace.numel() * workspace.element_size()
+        scratch = workspace.data_ptr()
     p = cache._packed + _pack(
         _ATTN, q.data_ptr(), o.data_ptr(), lse.data_ptr(), _ints(k_len, "k_len", B, dev), _ints(dev_status, "dev_status", 1, dev),
-        H, N, 1 if causal else 0, scale, fb.FA_O_BF16 if o_dtype is _BF16 else fb.FA_O_F32, workspace.data_ptr(), size,
+        H, N, 1 if causal else 0, scale, fb.FA_O_BF16 if o_dtype is _BF16 else fb.FA_O_F32, scratch, size,
         timeout_ms, test_drop_load)
     st = _call("fa_cache_attn")(p, _raw_stream(dev))
     if st:

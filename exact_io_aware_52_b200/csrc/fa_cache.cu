@@ -86,9 +86,37 @@ fa_status launch_append(const fa::AppendParams &kp, unsigned grid, int threads, 
 }
 
 // ---------------------------------------------------------------- attention
+constexpr int kMaxCluster = 8;
+// SMs of the GPU that the choice below is made for.  It does not ask the device, so that the scratch a call
+// needs follows from its sizes; on a smaller part of one the clusters take turns.
+constexpr int kSMs = 148;
+
+// CTAs (of `warps` warps) for each pair when clusters of them take the (sequence, head) pairs whole; 0: split the
+// keys of all pairs instead.  As many as leave a warp one tile of the tokens that a sequence can hold, fewer if not
+// all would run at once (clusters are sure of 7/8 of the SMs, for a cluster lies on one GPC).  Splitting
+// wins from about 5 tiles for a warp on, from 3 with more than 4 query rows.  Measured on B200, d = 128, 8
+// pairs of 4 rows: 512 tokens 7.1 us against 9.0, 2048 tokens 8.0 against 10.6, 8192 tokens 10.9 against 13.1.
+int direct_cluster(const fa_cache &c, int chunks, int nt, int warps) {
+    const long long units = (long long)c.B * c.H_kv * chunks;
+    const long long tiles = ((long long)c.max_pages * c.page) / fa::cattn::kTile;
+    int n = 1;
+    while (n < kMaxCluster && (long long)n * warps < tiles) n *= 2;
+    while (n > 1 && units * n > kSMs / 8 * 7) n /= 2;
+    return units * n <= kSMs && tiles <= (nt == 0 ? 4LL : 2LL) * n * warps ? n : 0;
+}
+
+int direct_warps(int d, int nt) {
+    namespace ca = fa::cattn;
+    if (d == 64) return nt < 2 ? ca::kDirectWarps<64, 1> : ca::kDirectWarps<64, 2>;
+    if (d == 128) return nt < 2 ? ca::kDirectWarps<128, 1> : ca::kDirectWarps<128, 2>;
+    return ca::kDirectWarps<256, 1>;
+}
+
 struct AttnPlan {
-    int nt, rows, chunks, workers;
-    size_t o_bytes, ml_bytes;
+    int nt, rows, chunks;
+    int cluster;              // CTAs for each pair, or 0 and
+    int workers;              // warps that split the keys, for each chunk
+    size_t o_bytes, ml_bytes; // their scratch
 };
 
 // CTAs that one SM holds (the kernel's launch bounds).
@@ -107,6 +135,10 @@ AttnPlan plan_attn(const fa_cache_attn_params *p, int resident) {
     a.nt = a.rows <= 4 ? 0 : ((a.rows <= 8 || c.d == 256) ? 1 : 2);
     const int per = ca::rows_of(a.nt);
     a.chunks = (a.rows + per - 1) / per;
+    a.cluster = direct_cluster(c, a.chunks, a.nt, direct_warps(c.d, a.nt));
+    a.workers = 0;
+    a.o_bytes = a.ml_bytes = 0;
+    if (a.cluster) return a;
     long long w = resident / a.chunks;
     const long long tiles = (long long)c.B * c.H_kv * (((long long)c.max_pages * c.page) / ca::kTile);
     if (w > tiles) w = tiles;  // a worker takes one at least
@@ -115,22 +147,6 @@ AttnPlan plan_attn(const fa_cache_attn_params *p, int resident) {
     a.o_bytes = slots * c.d * sizeof(float);
     a.ml_bytes = slots * 2 * sizeof(float);
     return a;
-}
-
-constexpr int kMaxCluster = 8;
-
-// CTAs (of `warps` warps) for each pair when clusters of them take the (sequence, head) pairs whole; 0: split the
-// keys of all pairs instead.  As many as leave a warp one tile of the tokens that a sequence can hold, fewer if not
-// all would run at once (clusters are sure of 7/8 of the SMs, for a cluster lies on one GPC).  Splitting
-// wins from about 5 tiles for a warp on, from 3 with more than 4 query rows.  Measured on B200, d = 128, 8
-// pairs of 4 rows: 512 tokens 7.1 us against 9.0, 2048 tokens 8.0 against 10.6, 8192 tokens 10.9 against 13.1.
-int direct_cluster(const fa::cattn::Params &kp, int warps, int most_tiles, int sms) {
-    const long long units = (long long)kp.c.B * kp.c.H_kv * kp.chunks;
-    const long long tiles = ((long long)kp.c.max_pages * kp.c.page) / fa::cattn::kTile;
-    int n = 1;
-    while (n < kMaxCluster && (long long)n * warps < tiles) n *= 2;
-    while (n > 1 && units * n > sms / 8 * 7) n /= 2;
-    return units * n <= sms && tiles <= (long long)most_tiles * n * warps ? n : 0;
 }
 
 bool attn_empty(const fa_cache_attn_params *p) {
@@ -169,11 +185,9 @@ template <int D, int NT>
 fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_t s) {
     namespace ca = fa::cattn;
     constexpr int W = ca::kDirectWarps<D, NT>;
-    if (const int n = direct_cluster(kp, W, NT == 0 ? 4 : 2, sms)) {
+    if (const int n = kp.cluster) {
         const fa_status st = set_attn_smem<D, NT, W>(dev);
         if (st != FA_OK) return st;
-        fa::cattn::Params dp = kp;
-        dp.cluster = n;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(kp.c.B * kp.c.H_kv * kp.chunks * n));
         cfg.blockDim = dim3(32 * W);
@@ -185,7 +199,7 @@ fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_
         at.val.clusterDim.y = at.val.clusterDim.z = 1;
         cfg.attrs = &at;
         cfg.numAttrs = n > 1 ? 1 : 0;
-        return cudaLaunchKernelEx(&cfg, ca::fa_cache_attn_kernel<D, NT, W>, dp) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, ca::fa_cache_attn_kernel<D, NT, W>, kp) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     }
     const fa_status st = set_attn_smem<D, NT, ca::kWarps>(dev);
     if (st != FA_OK) return st;
@@ -326,11 +340,12 @@ fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream) {
     // the kernels' line of (sequence, head) pairs is counted in 32 bits
     if ((long long)c.B * c.H_kv > kMaxInt / ((long long)c.max_pages * (c.page / fa::cattn::kTile) + fa::cattn::kPairCost))
         return FA_ERR_INVALID_ARGUMENT;
-    if (!p->q || !p->o || !p->lse || !p->k_len || !p->workspace) return FA_ERR_INVALID_ARGUMENT;
+    if (!p->q || !p->o || !p->lse || !p->k_len) return FA_ERR_INVALID_ARGUMENT;
     if (!aligned(p->q, 16) || !aligned(p->o, 16) || !aligned(p->workspace, 16) || !aligned(p->lse, 4) ||
         !aligned(p->k_len, 4) || !aligned(p->dev_status, 4))
         return FA_ERR_MISALIGNED;
-    if (p->workspace_bytes < fa_cache_attn_workspace_bytes(p)) return FA_ERR_INVALID_ARGUMENT;
+    const size_t scratch = fa_cache_attn_workspace_bytes(p);
+    if (scratch && (!p->workspace || p->workspace_bytes < scratch)) return FA_ERR_INVALID_ARGUMENT;
     int dev = 0, sms = 0;
     if ((st = fa_detail::current_device(&dev, &sms)) != FA_OK) return st;
 
@@ -351,6 +366,7 @@ fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream) {
     kp.rows = a.rows;
     kp.chunks = a.chunks;
     kp.workers = a.workers;
+    kp.cluster = a.cluster;
     kp.causal = p->causal;
     kp.o_bf16 = p->o_dtype == FA_O_BF16;
     kp.scale_log2 = (float)((double)p->scale * 1.4426950408889634074);
@@ -360,8 +376,8 @@ fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream) {
     const bool pages = c.n_pages > 0;
     const int line = c.d == 256 ? 256 : 128, lines = fa::cattn::kTile * c.d / line;
     const long long tiles = pages ? (long long)c.n_pages * c.H_kv * (c.page / fa::cattn::kTile) : 1;
-    if ((st = fa_detail::encode_cache_map(&kp.tm_k, pages ? c.k : p->workspace, tiles, lines, line)) != FA_OK ||
-        (st = fa_detail::encode_cache_map(&kp.tm_v, pages ? c.v : p->workspace, tiles, lines, line)) != FA_OK)
+    if ((st = fa_detail::encode_cache_map(&kp.tm_k, pages ? c.k : p->o, tiles, lines, line)) != FA_OK ||
+        (st = fa_detail::encode_cache_map(&kp.tm_v, pages ? c.v : p->o, tiles, lines, line)) != FA_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return c.d == 64 ? launch_attn_d<64>(kp, a.nt, dev, sms, s)

@@ -492,7 +492,8 @@ typedef struct {
                                   so that the wait for it runs out                       */
 } fa_cache_attn_params;
 
-/* Scratch bytes fa_cache_attn needs for *p; host arithmetic only; 0 for a NULL p. */
+/* Scratch bytes fa_cache_attn needs for *p; host arithmetic only; 0 for a NULL p, and where a few short
+ * sequences (by what the table can hold) need none. */
 FA_EXPORT size_t fa_cache_attn_workspace_bytes(const fa_cache_attn_params *p);
 
 /*

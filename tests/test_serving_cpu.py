@@ -166,7 +166,7 @@ def _gather_status(cache=None, **kw):
 
 
 def _attn_params(cache=None, **kw):
-    base = dict(cache=_cache(**(cache or {})), q=0x60000, o=0x70000, lse=0x80000, k_len=0x90000, H=8, N=1, causal=1,
+    base = dict(cache=_cache(**{"max_pages": 512, **(cache or {})}), q=0x60000, o=0x70000, lse=0x80000, k_len=0x90000, H=8, N=1, causal=1,
                 scale=0.1, o_dtype=0, workspace=0xa0000, workspace_bytes=1 << 30)
     base.update(kw)
     return fb.FaCacheAttnParams(**base)
@@ -232,11 +232,12 @@ def test_null_params():
 def test_attn_workspace_bytes():
     size = lambda cache=None, **kw: fb.load().fa_cache_attn_workspace_bytes(ctypes.byref(_attn_params(cache, **kw)))  # noqa: E731
     # one pair of slots of 4 or 8 rows for each worker, 2560 workers at most
-    assert 0 < size() <= 2560 * 2 * 4 * (128 + 2) * 4
-    assert size(dict(B=1, H_kv=1, max_pages=1), H=1) == 4 * 2 * 4 * (128 + 2) * 4   # 4 tiles: no more workers
-    assert size(dict(B=64, max_pages=128)) == 2560 * 2 * 4 * (128 + 2) * 4
-    assert size(dict(B=64, max_pages=128), H=16) == 2560 * 2 * 8 * (128 + 2) * 4
-    assert size(H=64) >= size(H=8)
+    assert size() == size(dict(B=64, max_pages=128)) == 2560 * 2 * 4 * (128 + 2) * 4
+    assert size(H=16) == 2560 * 2 * 8 * (128 + 2) * 4
+    # 1000 pairs with 2 tiles each: no more workers than tiles
+    assert size(dict(B=500, max_pages=2, page=16)) == 2000 * 2 * 4 * (128 + 2) * 4
+    # few sequences that can hold few tokens: none
+    assert size(dict(max_pages=8)) == size(dict(B=1, H_kv=1, max_pages=1), H=1) == 0
     assert size(H=0) == size(N=0) == size(H=3) == size(dict(page=5)) == size(dict(B=0)) == 0
     assert fb.status_string(fb.FA_ERR_BAD_PAGE) == "FA_ERR_BAD_PAGE"
 

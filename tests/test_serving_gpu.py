@@ -731,6 +731,7 @@ def test_graph_of_a_decoding_step():
 
 def test_binding_refusals_on_the_gpu():
     c = cache_of(ref.pool(45, [20], 2, 16, 64))
+    long = fa.PagedCache(c.k, c.v, c.k_scale, c.v_scale, c.table.repeat(1, 2000).contiguous())  # needs scratch
     x = torch.zeros(1, 2, 3, 64, dtype=BF16, device=dev())
     n = ints([0])
     r = fa.Rotary(64)
@@ -742,7 +743,7 @@ def test_binding_refusals_on_the_gpu():
         lambda: fa.cache_append(c, x.transpose(2, 3).contiguous().transpose(2, 3), x, n),
         lambda: fa.cache_attention(c, x.float(), n, True, 0.1), lambda: fa.cache_attention(c, x[:, :, ::2], n, True, 0.1),
         lambda: fa.cache_attention(c, x[:, :1], n, True, 0.1), lambda: fa.cache_attention(c, x, n, True, 0.1, out_dtype=torch.float16),
-        lambda: fa.cache_attention(c, x, n, True, -0.1), lambda: fa.cache_attention(c, x, n, True, 0.1, workspace=n),
+        lambda: fa.cache_attention(c, x, n, True, -0.1), lambda: fa.cache_attention(long, x, n, True, 0.1, workspace=n),
         lambda: fa.cache_attention(c, x, n, True, 0.1, out=(x, x)), lambda: fa.cache_gather(c, n, -1),
         lambda: fa.cache_gather(c, n, 4, out=(x, x)), lambda: fa.cache_gather(c, n.float(), 4),
         lambda: fa.rope(r, x, pos=torch.zeros(1, 3, device=dev())), lambda: fa.rope(r, x, pos=ints([0])),
