@@ -845,24 +845,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps<WPR>) fa_cache_merge_kernel(c
     float top = neg_inf(), sum = 0.f;
     for (int i0 = sub; i0 < n; i0 += 32 * WPR) {
         const int own = i0 + lane * WPR;
-        float2 ml = make_float2(neg_inf(), 0.f);
-        if (own < n) ml = p.ml_part[index(own)];
-        float t = fmaxf(ml.x, top);
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, i));
-        if (t != neg_inf()) {  // else nothing has been seen: there is nothing to rescale
-            const float f = ex2_approx(top - t);
-            sum *= f;
-#pragma unroll
-            for (int k = 0; k < W; ++k) o[k] *= f;
-        }
-        top = t;
-        const float a = ex2_approx(ml.x - (t == neg_inf() ? 0.f : t)) * ml.y;
-        sum += a;  // this lane's parts; the lanes are added at the end
         const int m = min((n - i0 + WPR - 1) / WPR, 32);
         constexpr int UN = W > 4 ? 4 : 8;
-        for (int j0 = 0; j0 < m; j0 += UN) {
-            float y[UN][W];
+        float y[UN][W];
+        auto load = [&](int j0) {
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
                 const float *src = p.o_part + index(i0 + min(j0 + u, m - 1) * WPR) * D + lane * W;
@@ -877,6 +863,24 @@ __global__ void __launch_bounds__(32 * kMergeWarps<WPR>) fa_cache_merge_kernel(c
                     y[u][0] = z.x, y[u][1] = z.y;
                 }
             }
+        };
+        float2 ml = make_float2(neg_inf(), 0.f);
+        if (own < n) ml = p.ml_part[index(own)];
+        load(0);  // in flight together with the statistics
+        float t = fmaxf(ml.x, top);
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, i));
+        if (t != neg_inf()) {  // else nothing has been seen: there is nothing to rescale
+            const float f = ex2_approx(top - t);
+            sum *= f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) o[k] *= f;
+        }
+        top = t;
+        const float a = ex2_approx(ml.x - (t == neg_inf() ? 0.f : t)) * ml.y;
+        sum += a;  // this lane's parts; the lanes are added at the end
+        for (int j0 = 0; j0 < m; j0 += UN) {
+            if (j0 > 0) load(j0);
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
                 if (j0 + u >= m) break;

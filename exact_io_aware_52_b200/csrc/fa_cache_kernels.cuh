@@ -64,8 +64,11 @@ __device__ __forceinline__ uint32_t codes4(const float *v, float inv) {
     if constexpr (SPECIAL)
         return pack_e4m3x4(fmaf(v[0], inv, v[0] * 0.f), fmaf(v[1], inv, v[1] * 0.f), fmaf(v[2], inv, v[2] * 0.f),
                            fmaf(v[3], inv, v[3] * 0.f));
-    else
-        return pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    else {
+        const float2 i2 = make_float2(inv, inv);
+        const float2 a = __fmul2_rn(make_float2(v[0], v[1]), i2), b = __fmul2_rn(make_float2(v[2], v[3]), i2);
+        return pack_e4m3x4(a.x, a.y, b.x, b.y);
+    }
 }
 
 // The four values of a word of E4M3 codes.
