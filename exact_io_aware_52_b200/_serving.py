@@ -174,9 +174,11 @@ def rope(rotary, q, k=None, *, pos=None, pos0=0, inverse=False, out_dtype=None, 
         y_dtype = yq.dtype
         for x, y in ((q, yq), (k, yk)):
             if x is not None:
-                _heads(y, "out", dev)
+                sy = _heads(y, "out", dev)
                 if y.shape != x.shape or y.dtype is not y_dtype:
                     _refuse("out must have its input's shape, and both the same dtype")
+                if 0 in sy and any(n > 1 and st == 0 for n, st in zip(y.shape, sy)):
+                    _refuse("out must not be expanded")
         if out_dtype is not None and out_dtype is not y_dtype:
             _refuse("out must be of out_dtype")
     y_type = _DTYPES.get(y_dtype)
@@ -255,7 +257,8 @@ def cache_append(cache, k, v, start, *, n_new=None, rotary=None, dev_status=None
     k, v: bf16 [B, H_kv, N, d], any strides with contiguous components.  start:
     int32 [B], the tokens that each sequence holds already.  n_new: int32 [B], how many of
     its N tokens are written (default: all).  rotary turns the keys by their
-    positions on the way.  dev_status: int32 status word for FA_ERR_BAD_PAGE.
+    positions on the way.  dev_status: int32 status word for FA_ERR_BAD_PAGE.  No page may be
+    written through two entries of the table in one call.
     """
     dev = cache.device_index
     sk, sv = _heads(k, "k", dev), _heads(v, "v", dev)
@@ -287,8 +290,8 @@ def cache_gather(cache, k_len, N_k, *, out=None, dev_status=None, stream=None):
     attention(..., k_len=k_len) reads.  out: a pair of such tensors to write."""
     dev = cache.device_index
     N_k = int(N_k)
-    if N_k < 0:
-        _refuse("N_k must not be negative")
+    if not 0 <= N_k < 1 << 31:
+        _refuse("N_k must be in [0, 2^31)")
     shape = (cache.B, cache.H_kv, N_k, cache.d)
     if out is not None:
         for t in out:

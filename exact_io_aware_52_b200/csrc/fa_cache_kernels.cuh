@@ -411,9 +411,10 @@ __global__ void __launch_bounds__(32 * kFewWarps) fa_cache_append_few_kernel(con
         load8(xk + at.b, k + 8);
         w.load(xv, plain_slot(slot));
         if (at.rotated) {
+            const int pos = (int)((unsigned)start + i);  // (past the table where this wraps)
             float cs[8], sn[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) rotary_cs(p.step[rotary_pair(slot, j, p.dim, p.interleaved)], start + i, p.amplitude, 1.f, cs[j], sn[j]);
+            for (int j = 0; j < 8; ++j) rotary_cs(p.step[rotary_pair(slot, j, p.dim, p.interleaved)], pos, p.amplitude, 1.f, cs[j], sn[j]);
             rotary_turn_slot(k, cs, sn, p.interleaved);
         }
     }

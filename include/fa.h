@@ -443,7 +443,7 @@ typedef struct {
  *
  * A token whose position is negative or past the table, or whose page is
  * outside [0, n_pages), is not written and FA_ERR_BAD_PAGE is stored in
- * *dev_status.  Two sequences must not append to the same page in one call.
+ * *dev_status.  No page may be written through two entries of the table in one call.
  */
 FA_EXPORT fa_status fa_cache_append(const fa_cache_append_params *p, void *stream);
 

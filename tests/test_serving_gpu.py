@@ -582,6 +582,50 @@ def test_attention_wait_that_runs_out(d, drop):
     check_attention(o, lse, q, pool, lens, True, 0.1, 16)
 
 
+def test_attention_without_any_page():
+    q = torch.randn(2, 4, 1, 64, generator=torch.Generator().manual_seed(16)).to(BF16)
+    none = torch.zeros(0, 2, 16, 64, dtype=torch.uint8, device=dev()), torch.zeros(0, 2, device=dev())
+    for table in (torch.zeros(2, 5), torch.full((2, 3000), -1.0)):
+        c = fa.PagedCache(none[0], none[0], none[1], none[1], table.to(torch.int32).to(dev()))
+        o, lse = run_attention(q, None, [70, 0], True, 0.1, cache=c, status_want=fb.FA_ERR_BAD_PAGE)
+        assert (o == 0).all() and torch.isneginf(lse).all()
+        status = ints([0])
+        k, v = fa.cache_gather(c, ints([70, 0]), 70, dev_status=status)
+        assert fa.read_device_status(status) == fb.FA_ERR_BAD_PAGE and (k == 0).all() and (v == 0).all()
+        status.zero_()
+        x = torch.zeros(2, 2, 3, 64, dtype=BF16, device=dev())
+        fa.cache_append(c, x, x, ints([0, 0]), dev_status=status)
+        assert fa.read_device_status(status) == fb.FA_ERR_BAD_PAGE
+    # a table without columns: sequences without tokens, for few pairs and for many
+    for B in (2, 200):
+        kv = torch.zeros(1, 2, 16, 64, dtype=torch.uint8, device=dev())
+        one = torch.ones(1, 2, device=dev())
+        c = fa.PagedCache(kv, kv, one, one, torch.zeros(B, 0, dtype=torch.int32, device=dev()))
+        o, lse = run_attention(q[:1].expand(B, 4, 1, 64).contiguous(), None, [9] * B, True, 0.1, cache=c)
+        assert (o == 0).all() and torch.isneginf(lse).all()
+    # no sequences, no queries
+    c = fa.PagedCache(kv, kv, one, one, torch.zeros(0, 3, dtype=torch.int32, device=dev()))
+    n = torch.zeros(0, dtype=torch.int32, device=dev())
+    o, lse = fa.cache_attention(c, torch.zeros(0, 4, 1, 64, dtype=BF16, device=dev()), n, True, 0.1)
+    assert o.shape == (0, 4, 1, 64) and lse.shape == (0, 4, 1)
+    assert fa.cache_gather(c, n, 5)[0].shape == (0, 2, 5, 64)
+    fa.cache_append(c, torch.zeros(0, 2, 1, 64, dtype=BF16, device=dev()), torch.zeros(0, 2, 1, 64, dtype=BF16, device=dev()), n)
+
+
+@pytest.mark.parametrize("B", [33, 257])
+def test_attention_many_sequences(B):
+    """More sequences than a warp has lanes, most of them short or empty."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 40, (B,), generator=g).tolist()
+    lens[B // 2], lens[-1] = 900, 0
+    pool = ref.pool(B, lens, 1, 32, 64)
+    wide = (*pool[:4], torch.cat([pool[4], torch.full((B, 400), -1, dtype=torch.int32)], 1))
+    q = torch.randn(B, 4, 1, 64, generator=g).to(BF16)
+    for p in (pool, wide):
+        o, lse = run_attention(q, p, lens, True, 0.125)
+        check_attention(o, lse, q, p, lens, True, 0.125, 32)
+
+
 def test_attention_shared_pages_length_past_the_table_and_strided_table():
     page, d = 32, 128
     pool = ref.pool(39, [200], 2, page, d)
@@ -692,12 +736,15 @@ def test_results_do_not_depend_on_timing_or_stream():
         assert torch.equal(a, o) and torch.equal(b, lse)
 
 
-def test_graph_of_a_decoding_step():
+@pytest.mark.parametrize("room", [1, 1000])  # clusters; split keys and their merge
+def test_graph_of_a_decoding_step(room):
     """One captured step, replayed for growing lengths that only the device knows."""
     B, H, H_kv, d, page = 2, 4, 2, 64, 16
     pool = ref.pool(44, [60, 60], H_kv, page, d)
+    pool = (*pool[:4], torch.cat([pool[4]] + [torch.full_like(pool[4], -1)] * (room - 1), 1))
     dpool = to_gpu(pool)
     c = fa.PagedCache(*dpool)
+    assert (fa.cache_attention_workspace_bytes(c, H, 1) == 0) == (room == 1)
     rot = fa.Rotary(d)
     x = torch.zeros(B, 1, H + 2 * H_kv, d, dtype=BF16, device=dev())
     q, k, v = (t.transpose(1, 2) for t in (x[:, :, :H], x[:, :, H:H + H_kv], x[:, :, H + H_kv:]))
@@ -749,7 +796,9 @@ def test_binding_refusals_on_the_gpu():
         lambda: fa.rope(r, x, pos=torch.zeros(1, 3, device=dev())), lambda: fa.rope(r, x, pos=ints([0])),
         lambda: fa.rope(r, x, x[:, :, :1]), lambda: fa.rope(r, x.half()), lambda: fa.rope(r, x, out=x[:, :, :2]),
         lambda: fa.rope(r, x, x.float()), lambda: fa.rope(r, x[0]), lambda: fa.rope(fa.Rotary(128), x),
-        lambda: fa.rope(r, x, out=x.float(), out_dtype=BF16),
+        lambda: fa.rope(r, x, out=x.float(), out_dtype=BF16), lambda: fa.rope(r, x, out=x[:, :1].clone().expand(1, 2, 3, 64)),
+        lambda: fa.rope(r, x, pos0=1 << 40), lambda: fa.cache_gather(c, n, 1 << 40), lambda: fa.cache_attention(c, x, n, True, 1e60),
+        lambda: fa.cache_attention(c, x, n, True, 0.1, timeout_ms=-1),
         lambda: fa.PagedCache(c.k[:, :, ::2], c.v[:, :, ::2], c.k_scale, c.v_scale, c.table),
         lambda: fa.PagedCache(c.k, c.v[:2], c.k_scale, c.v_scale, c.table),
         lambda: fa.PagedCache(c.k, c.v, c.k_scale.double(), c.v_scale, c.table),
