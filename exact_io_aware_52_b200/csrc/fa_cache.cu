@@ -69,13 +69,13 @@ bool vectors(const void *base, const int64_t *stride, int B, int H, int N) {
     return true;
 }
 
-template <int SPT, bool VEC>
-fa_status launch_append(const fa::AppendParams &kp, unsigned grid, int threads, int dev, cudaStream_t s) {
+template <bool VEC, bool TWO>
+fa_status launch_append(const fa::AppendParams &kp, int tokens, unsigned grid, int threads, int dev, cudaStream_t s) {
     static std::atomic<bool> ready[kMaxDevices];
-    auto kern = fa::fa_cache_append_kernel<SPT, VEC>;
-    // the sines and cosines of a page's tokens: 8 bytes for each pair
-    const int smem = VEC ? kp.c.page * (kp.dim / 2) * 8 : 0;
-    if (smem > 48 * 1024 && !ready[dev].load(std::memory_order_acquire)) {
+    auto kern = fa::fa_cache_append_kernel<VEC, TWO>;
+    // the sines and cosines of a page's new tokens: 8 bytes for each pair
+    const int smem = VEC ? tokens * (kp.dim / 2) * 8 : 0;
+    if (smem > 46 * 1024 && !ready[dev].load(std::memory_order_acquire)) {  // (2 KB are the kernel's own)
         constexpr int most = 128 * (FA_ROTARY_MAX_DIM / 2) * 8;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
             return FA_ERR_CUDA;
@@ -274,8 +274,11 @@ fa_status fa_cache_append(const fa_cache_append_params *p, void *stream) {
         fa::fa_cache_append_few_kernel<<<(unsigned)blocks, 32 * fa::kFewWarps, 0, s>>>(kp);
         return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     }
-    const int slots = c.page * (c.d / 16);  // 64 .. 2048 of 16 components
-    const int threads = slots < 512 ? slots : 512;
+    // slots of 16 components of as many new tokens as a page can get: a power of two, at most 2048
+    int tokens = 1;
+    while (tokens < c.page && tokens < p->N) tokens *= 2;
+    const int slots = tokens * (c.d / 16);
+    const int threads = slots < 32 ? 32 : (slots < 1024 ? slots : 1024);
     // as many heads in a block, which share the sines, as leave every SM 2048 threads in all
     const long long touched = (long long)c.B * kp.pages;
     kp.group = c.H_kv;
@@ -284,11 +287,11 @@ fa_status fa_cache_append(const fa_cache_append_params *p, void *stream) {
     const long long blocks = touched * ((c.H_kv + kp.group - 1) / kp.group);
     if (blocks > kMaxInt) return FA_ERR_INVALID_ARGUMENT;
     const unsigned grid = (unsigned)blocks;
-    switch (slots / threads) {
-        case 1: return vec ? launch_append<1, true>(kp, grid, threads, dev, s) : launch_append<1, false>(kp, grid, threads, dev, s);
-        case 2: return vec ? launch_append<2, true>(kp, grid, threads, dev, s) : launch_append<2, false>(kp, grid, threads, dev, s);
-        default: return vec ? launch_append<4, true>(kp, grid, threads, dev, s) : launch_append<4, false>(kp, grid, threads, dev, s);
-    }
+    if (slots > 1024)
+        return vec ? launch_append<true, true>(kp, tokens, grid, threads, dev, s)
+                   : launch_append<false, true>(kp, tokens, grid, threads, dev, s);
+    return vec ? launch_append<true, false>(kp, tokens, grid, threads, dev, s)
+               : launch_append<false, false>(kp, tokens, grid, threads, dev, s);
 }
 
 fa_status fa_cache_gather(const fa_cache_gather_params *p, void *stream) {

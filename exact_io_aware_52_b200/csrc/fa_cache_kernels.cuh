@@ -234,15 +234,17 @@ __device__ __forceinline__ void rescale_run(uint8_t *run, float ratio) {
 // its heads, so that nothing needs atomics and no order of blocks changes the result.
 // The sines and cosines, several times the work of the rest, are computed once for a group
 // and lie in shared memory (registers would leave no room for the next
-// head's loads, which are in flight while a head is finished).  A head's keys and
-// values are read once and stay in registers between the maximum and the rounding; a
-// thread has the same SPT slots (16 components of a token) of every head.  Bound by
+// head's loads, which are in flight while a head is finished).  A thread has the same slot
+// (16 components) of a new token for every head; keys and values are read once and stay in
+// registers between the maximum and the rounding.  TWO: a page's new tokens are two
+// blocks' worth of slots; they are read again, from L2, after the maximum.  Bound by
 // memory: 2 bytes read and 1 written per component.
-template <int SPT, bool VEC>
-__global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
+template <bool VEC, bool TWO>
+__global__ void __launch_bounds__(1024, 1) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
     extern __shared__ float4 s_cs[];  // [token][pair of entries][slot]: (cos, sin) of two of a slot's 8 entries
-    __shared__ uint2 s_max[2][16];
-    constexpr bool AHEAD = VEC && SPT <= 2;
+    __shared__ uint2 s_max[2][32];
+    constexpr bool AHEAD = VEC && !TWO;
+    constexpr int CHUNKS = TWO ? 2 : 1;
     const CacheView &c = p.c;
     const int groups = (c.H_kv + p.group - 1) / p.group;
     const int h0 = (blockIdx.x % groups) * p.group, h1 = min(h0 + p.group, c.H_kv);
@@ -253,84 +255,85 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
     const int dim = VEC ? p.dim : 0;
     const int per_row = c.d >> 4, row_log2 = 31 - __clz(per_row);
     const int turned = dim >> 4;  // slots of a token that are turned
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    // This thread's first slot: token t, and where it lies in the inputs and in the page; its i-th one is
-    // `dt` tokens further on.  All of them advance by a head at a time.
-    const int t = threadIdx.x >> row_log2, dt = blockDim.x >> row_log2, slot = threadIdx.x & (per_row - 1);
+    const int n_new = pg.s1 - pg.s0;
+    // This thread's slot of new token i of the page (and of token i + dt), and where it lies in the inputs
+    // and in the page.  All of it advances by a head at a time.
+    const int i = threadIdx.x >> row_log2, dt = blockDim.x >> row_log2, slot = threadIdx.x & (per_row - 1);
     const RotarySlot at = VEC ? rotary_slot(slot, c.d, dim) : plain_slot(slot);
     const bool turns = slot < turned;
-    const uint16_t *xk = p.x[0] + b * p.xs[0][0] + h0 * p.xs[0][1] + (pg.t0 - pg.s0 + t) * p.xs[0][2];
-    const uint16_t *xv = p.x[1] + b * p.xs[1][0] + h0 * p.xs[1][1] + (pg.t0 - pg.s0 + t) * p.xs[1][2] + 16 * slot;
-    const long long unit0 = (long long)pg.page_id * c.H_kv + h0;
-    uint8_t *ck = c.k + (unit0 * c.page + t) * c.d, *cvv = c.v + (unit0 * c.page + t) * c.d + 16 * slot;
-    float *sk = c.k_scale + unit0, *sv = c.v_scale + unit0;
+    const uint16_t *xk = p.x[0] + b * p.xs[0][0] + h0 * p.xs[0][1] + (pg.t0 + i) * p.xs[0][2];
+    const uint16_t *xv = p.x[1] + b * p.xs[1][0] + h0 * p.xs[1][1] + (pg.t0 + i) * p.xs[1][2] + 16 * slot;
+    int unit = pg.page_id * c.H_kv + h0;  // (page, head)
+    long long off = ((long long)unit * c.page + pg.s0 + i) * c.d;
 
-    Raw16 rk[SPT], rv[SPT];
-    // This thread's slots of the head at xk, xv.
-    auto load = [&]() {
-#pragma unroll
-        for (int i = 0; i < SPT; ++i) {
-            const int ti = t + i * dt;
-            if (ti < pg.s0 || ti >= pg.s1) continue;
-            if constexpr (VEC) {
-                rk[i].load(xk + i * dt * p.xs[0][2], at);
-                rv[i].load(xv + i * dt * p.xs[1][2], RotarySlot{0, 8, false});
-            } else {
-                rv[i].load_elements(xv + i * dt * p.xs[1][2]);
-            }
+    Raw16 rk, rv;
+    auto load = [&](int chunk) {
+        if (i + chunk * dt >= n_new) return;
+        if constexpr (VEC) {
+            rk.load(xk + chunk * dt * p.xs[0][2], at);
+            rv.load(xv + chunk * dt * p.xs[1][2], RotarySlot{0, 8, false});
+        } else {
+            rv.load_elements(xv + chunk * dt * p.xs[1][2]);
         }
     };
-    load();
+    load(0);
     if constexpr (VEC) {
         if (dim) {
             __shared__ uint64_t step[FA_ROTARY_MAX_DIM / 2];
-            for (int i = threadIdx.x; i < (dim >> 1); i += blockDim.x) step[i] = p.step[i];
+            for (int j = threadIdx.x; j < (dim >> 1); j += blockDim.x) step[j] = p.step[j];
             __syncthreads();
-            const unsigned n = (pg.s1 - pg.s0) * 4 * turned;
+            const unsigned n = n_new * 4 * turned;
             for (unsigned k = threadIdx.x; k < n; k += blockDim.x) {
                 const unsigned q = k / (unsigned)turned, e = k - q * turned;
-                const int tok = pg.s0 + (q >> 2), j = 2 * (q & 3);
+                const int pos = (int)(pg.lo + pg.s0 + (q >> 2)), j = 2 * (q & 3);
                 float4 x;
-                rotary_cs(step[rotary_pair(e, j, dim, p.interleaved)], (int)(pg.lo + tok), p.amplitude, 1.f, x.x, x.y);
-                rotary_cs(step[rotary_pair(e, j + 1, dim, p.interleaved)], (int)(pg.lo + tok), p.amplitude, 1.f, x.z, x.w);
-                s_cs[(tok * 4 + (q & 3)) * turned + e] = x;
+                rotary_cs(step[rotary_pair(e, j, dim, p.interleaved)], pos, p.amplitude, 1.f, x.x, x.y);
+                rotary_cs(step[rotary_pair(e, j + 1, dim, p.interleaved)], pos, p.amplitude, 1.f, x.z, x.w);
+                s_cs[q * turned + e] = x;
             }
             __syncthreads();
         }
     }
+    const float4 *my_cs = s_cs + i * 4 * turned + slot;
+    // The key of this thread's slot, turned.
+    auto key = [&](int chunk, float (&k)[16]) {
+        if constexpr (VEC) {
+            rk.get(k);
+            if (turns) {
+                float cs[8], sn[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 x = my_cs[(chunk * dt * 4 + j) * turned];
+                    cs[2 * j] = x.x, sn[2 * j] = x.y, cs[2 * j + 1] = x.z, sn[2 * j + 1] = x.w;
+                }
+                rotary_turn_slot(k, cs, sn, p.interleaved);
+            }
+        } else {
+            for (int j = 0; j < 16; ++j)
+                k[j] = key_component(p, xk + chunk * dt * p.xs[0][2], 16 * slot + j, (int)(pg.lo + pg.s0 + i + chunk * dt));
+        }
+    };
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 
-    const float4 *my_cs = s_cs + t * 4 * turned + slot;
     for (int h = h0; h < h1; ++h) {
-        if (!AHEAD && h > h0) load();
-        float k[SPT][16];
-        Raw16 v[SPT];
+        float k[16];
+        Raw16 v;
         uint32_t mk = 0, mv = 0;
 #pragma unroll
-        for (int i = 0; i < SPT; ++i) {
-            const int ti = t + i * dt;
-            if (ti < pg.s0 || ti >= pg.s1) continue;
-            v[i] = rv[i];
-            if constexpr (VEC) {
-                rk[i].get(k[i]);
-                if (turns) {
-                    float cs[8], sn[8];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 x = my_cs[(i * dt * 4 + j) * turned];
-                        cs[2 * j] = x.x, sn[2 * j] = x.y, cs[2 * j + 1] = x.z, sn[2 * j + 1] = x.w;
-                    }
-                    rotary_turn_slot(k[i], cs, sn, p.interleaved);
-                }
-            } else {
-                for (int j = 0; j < 16; ++j)
-                    k[i][j] = key_component(p, xk + i * dt * p.xs[0][2], 16 * slot + j, (int)(pg.lo + ti));
+        for (int chunk = 0; chunk < CHUNKS; ++chunk) {
+            if (TWO || (!AHEAD && h > h0)) load(chunk);
+            if (i + chunk * dt < n_new) {
+                v = rv;
+                key(chunk, k);
+                mk = max(mk, key_amax(k));
+                mv = max(mv, value_amax(v));
             }
-            mk = max(mk, key_amax(k[i]));
-            mv = max(mv, value_amax(v[i]));
         }
-        xk += p.xs[0][1];
-        xv += p.xs[1][1];
-        if (AHEAD && h + 1 < h1) load();
+        if (AHEAD) {
+            xk += p.xs[0][1];
+            xv += p.xs[1][1];
+            if (h + 1 < h1) load(0);
+        }
         uint2 *sm = s_max[h & 1];  // the other one may still be read for the head before
         auto block_max = [&]() {
             mk = __reduce_max_sync(0xffffffffu, mk);
@@ -342,18 +345,22 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
             mv = __reduce_max_sync(0xffffffffu, x.y);
         };
         // read by all before thread 0 writes them
-        const float before_k = pg.s0 > 0 ? *sk : 0.f, before_v = pg.s0 > 0 ? *sv : 0.f;
+        const float before_k = pg.s0 > 0 ? c.k_scale[unit] : 0.f, before_v = pg.s0 > 0 ? c.v_scale[unit] : 0.f;
         block_max();
         const bool special_k = mk >= kInfBits, special_v = mv >= kInfBits;
         if (special_k || special_v) {  // rare; the same for the whole block
             mk = mv = 0;
 #pragma unroll
-            for (int i = 0; i < SPT; ++i) {
-                const int ti = t + i * dt;
-                if (ti < pg.s0 || ti >= pg.s1) continue;
+            for (int chunk = 0; chunk < CHUNKS; ++chunk) {
+                if (i + chunk * dt >= n_new) continue;
+                if constexpr (TWO) {
+                    load(chunk);
+                    v = rv;
+                    key(chunk, k);
+                }
                 float y[16];
-                v[i].get(y);
-                mk = max(mk, amax_finite(k[i]));
+                v.get(y);
+                mk = max(mk, amax_finite(k));
                 mv = max(mv, amax_finite(y));
             }
             __syncthreads();
@@ -361,27 +368,37 @@ __global__ void __launch_bounds__(512, SPT == 1 ? 2 : 1) fa_cache_append_kernel(
         }
         const ScaleUpdate uk = update_scale(pg.s0 > 0, before_k, mk), uv = update_scale(pg.s0 > 0, before_v, mv);
 #pragma unroll
-        for (int i = 0; i < SPT; ++i) {
-            const int ti = t + i * dt;
-            if (ti >= pg.s1) continue;
-            if (ti >= pg.s0) {
-                float y[16];
-                v[i].get(y);
-                store_slot(ck + i * dt * c.d, at, k[i], uk.inv, special_k);
-                store_slot(cvv + i * dt * c.d, RotarySlot{0, 8, false}, y, uv.inv, special_v);
-            } else {  // exact ratios for powers of two
-                if (uk.grows) rescale_run(ck + i * dt * c.d + 16 * slot, before_k * uk.inv);
-                if (uv.grows) rescale_run(cvv + i * dt * c.d, before_v * uv.inv);
+        for (int chunk = 0; chunk < CHUNKS; ++chunk) {
+            if (i + chunk * dt >= n_new) continue;
+            if constexpr (TWO) {
+                load(chunk);
+                v = rv;
+                key(chunk, k);
             }
+            float y[16];
+            v.get(y);
+            store_slot(c.k + off + chunk * dt * c.d, at, k, uk.inv, special_k);
+            store_slot(c.v + off + chunk * dt * c.d, plain_slot(slot), y, uv.inv, special_v);
+        }
+        // the tokens from before, by exact ratios for powers of two
+        if (uk.grows) {
+            uint8_t *page = c.k + (long long)unit * c.page * c.d;
+            for (int r = threadIdx.x; r < pg.s0 * per_row; r += blockDim.x) rescale_run(page + 16 * r, before_k * uk.inv);
+        }
+        if (uv.grows) {
+            uint8_t *page = c.v + (long long)unit * c.page * c.d;
+            for (int r = threadIdx.x; r < pg.s0 * per_row; r += blockDim.x) rescale_run(page + 16 * r, before_v * uv.inv);
         }
         if (threadIdx.x == 0) {
-            if (pg.s0 == 0 || uk.grows) *sk = uk.now;
-            if (pg.s0 == 0 || uv.grows) *sv = uv.now;
+            if (pg.s0 == 0 || uk.grows) c.k_scale[unit] = uk.now;
+            if (pg.s0 == 0 || uv.grows) c.v_scale[unit] = uv.now;
         }
-        ck += c.page * c.d;
-        cvv += c.page * c.d;
-        ++sk;
-        ++sv;
+        if (!AHEAD) {
+            xk += p.xs[0][1];
+            xv += p.xs[1][1];
+        }
+        off += c.page * c.d;
+        ++unit;
     }
 }
 
