@@ -92,17 +92,23 @@ constexpr int kMaxCluster = 8;
 constexpr int kSMs = 148;
 
 // CTAs (of `warps` warps) for each pair when clusters of them take the (sequence, head) pairs whole; 0: split the
-// keys of all pairs instead.  As many as leave a warp one tile of the tokens that a sequence can hold, fewer if not
-// all would run at once (clusters are sure of 7/8 of the SMs, for a cluster lies on one GPC).  Splitting
-// wins from about 5 tiles for a warp on, from 3 with more than 4 query rows.  Measured on B200, d = 128, 8
-// pairs of 4 rows: 512 tokens 7.1 us against 9.0, 2048 tokens 8.0 against 10.6, 8192 tokens 10.9 against 13.1.
+// keys of all pairs instead.  One CTA up to two tiles for a warp, of the tokens that a sequence can hold; more of
+// them for one tile each, as long as all run at once (a cluster lies on one GPC, so that clusters of 4
+// and 8 are sure of 7/8 of the SMs only).  Splitting costs a second launch and the parts' way through memory,
+// and wins where a warp has more tiles than below, or where there are more than two rounds of CTAs.
+// Measured on B200, d = 128, split against clusters, us: 4 rows, 8 pairs of 512, 2048 and 8192 tokens 9.0 / 7.1,
+// 10.6 / 8.0, 13.1 / 10.9; 256 pairs of 200 14.5 / 10.4; 8 rows, 64 pairs of 1000 12.4 / 9.8; 16 rows, 128 pairs of
+// 300 and 600 22.1 / 9.4, 27.5 / 11.6; 3 pairs of 8000, 8 tiles for a warp, 14.3 / 17.9; 512 pairs of 56
+// rows and 300 tokens (four blocks of rows each) 22.3 / 29.2 in more than two rounds.
 int direct_cluster(const fa_cache &c, int chunks, int nt, int warps) {
     const long long units = (long long)c.B * c.H_kv * chunks;
     const long long tiles = ((long long)c.max_pages * c.page) / fa::cattn::kTile;
     int n = 1;
-    while (n < kMaxCluster && (long long)n * warps < tiles) n *= 2;
-    while (n > 1 && units * n > kSMs / 8 * 7) n /= 2;
-    return units * n <= kSMs && tiles <= (nt == 0 ? 4LL : 2LL) * n * warps ? n : 0;
+    if (tiles > 2 * warps)
+        while (n < kMaxCluster && (long long)n * warps < tiles) n *= 2;
+    while (n > 1 && units * n > (n == 2 ? kSMs : kSMs / 8 * 7)) n /= 2;
+    const int most = units < 8 ? (nt == 0 ? 4 : 2) : (nt == 0 ? 6 : 8);  // few pairs leave SMs idle
+    return units * n <= 2 * kSMs && tiles <= (long long)most * n * warps ? n : 0;
 }
 
 int direct_warps(int d, int nt) {

@@ -422,6 +422,8 @@ ATTN_SHAPES = [  # H, H_kv, N, d, page, lens
     (6, 2, 5, 64, 16, [3, 5, 100, 0]), (16, 2, 1, 256, 32, [33, 700]), (32, 4, 2, 128, 128, [1000, 5, 129]),
     (12, 1, 7, 64, 64, [64, 300]), (8, 1, 7, 256, 16, [90]), (24, 3, 7, 128, 32, [31, 260, 2]), (4, 4, 130, 64, 64, [130, 200, 60]),
     (3, 1, 1, 128, 128, [9000]), (5, 5, 3, 256, 64, [1, 2, 3, 4, 63, 64, 65, 66]),
+    (17, 1, 1, 128, 64, [300, 9000]), (8, 1, 4, 64, 32, [64, 3, 7000]), (11, 1, 3, 128, 16, [40, 0, 2]), (4, 1, 9, 256, 128, [130, 4000]),
+    (8, 1, 8, 128, 128, [5000, 20]), (10, 2, 4, 64, 16, [100] * 40),
 ]
 
 
