@@ -178,6 +178,16 @@ __device__ __forceinline__ void locate(const Params &p, const Plan &plan, int x,
     }
 }
 
+// tma_load_3d with the destination as a shared-memory address.
+__device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
+                                               int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 r;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));

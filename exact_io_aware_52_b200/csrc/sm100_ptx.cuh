@@ -106,16 +106,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
-// The same with the destination as a shared-memory address.
-__device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
-                                               int c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
 // Element-wise add of a shared-memory tile into global memory through a
 // tensor map (TMA reduce, fp32 add for an fp32 map), tracked by the issuing
 // thread's bulk async-group.  Out-of-range rows of the box are skipped.
