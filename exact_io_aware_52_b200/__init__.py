@@ -2,7 +2,8 @@
 
 The hot path lives in ``csrc/`` (hand-written sm_100a CUDA built into
 ``libfa_sm100.so``, C ABI in ``include/fa.h``); this package is a thin ctypes
-binding over that library plus the seeded workload generator.  Nothing here
+binding over that library plus the seeded workload generator.  ``_serving.py``
+has rotary positions and the paged 8-bit key/value cache.  Nothing here
 computes attention on the CPU: when the library is missing, calls fail loudly.
 """
 from ._binding import (  # noqa: F401

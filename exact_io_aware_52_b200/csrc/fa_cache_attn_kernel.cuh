@@ -61,8 +61,9 @@ template <int D, int NT> constexpr int kResident = D == 64 ? (NT == 2 ? 3 : 4) :
 template <int D> constexpr int kStageBytes = 2 * kTile * D;  // codes of K and V
 template <int D> constexpr int kRingBytes = kStages<D> * kStageBytes<D>;
 template <int D, int WARPS> constexpr int kSmemBytes = WARPS * kRingBytes<D> + 1024;  // the rings begin on a swizzle atom
-// tau: three bits for each of 8 rows, every fourth bit left out.  d = 64 has two tokens in a
-// 128-byte line, the others one (or half of one).
+// tau(r) in four bits for each of 8 rows r: found by trying the orders for one in which neither the
+// lanes' reads of K (16 bytes) nor those of V (16, or 8 for d = 64) meet in a bank.  d = 64 has two
+// tokens in a 128-byte line, d = 256 half a token.
 template <int D> constexpr uint32_t kTau = D == 64 ? 0x65217430u : 0x37621540u;
 template <int D>
 __device__ __forceinline__ int tau(int r) { return (kTau<D> >> (4 * r)) & 7; }
@@ -101,7 +102,7 @@ __device__ __forceinline__ int seq_tiles(const Params &p, int b) { return (seq_l
 
 // All threads of a cluster's CTAs; what they wrote to shared memory before is visible to the others after.
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // Two floats of CTA `rank` of the cluster, at the place of this CTA's shared-memory address.
 __device__ __forceinline__ float2 peer_float2(uint32_t addr, int rank) {
@@ -226,7 +227,7 @@ __device__ __forceinline__ uint32_t transposed8x8(uint32_t a) {
     return r;
 }
 
-// Words of V codes of one lane: [token][word], tokens 2c, 2c + 1, 2c + 8, 2c + 9 of the tile.
+// Words of V codes of one lane: [token][word], tokens tau(2c), tau(2c + 1) of the tile and those 8 further on.
 template <int D> using VWords = uint32_t[4][D / 32];
 
 // The A operands of word w: matrix tile 2 w + i has the components 4 w + 2 i
@@ -293,8 +294,8 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     }
     __syncwarp();
     const CacheView &cv = p.c;
-    // this lane's places in a tile: runs j and j + 1 (d >= 128) of key tau(g) (+ 8 tokens: + 8 d
-    // bytes, for d = 64 in the other half of the line's chunks), and of values tau(2c), tau(2c + 1)
+    // This lane's places in a tile: its first run of key tau(g), and its run of the values tau(2c) and
+    // tau(2c + 1).  8 tokens further on are 8 lines (d = 64: 4 lines, which flips a bit of the swizzle).
     const uint32_t k_at = ring + swizzled(tau<D>(g) * (D == 64 ? 64 : 128) + 16 * c);
     const uint32_t v_at0 = ring + kTile * D + swizzled(tau<D>(2 * c) * (D == 64 ? 64 : 128) + (D == 64 ? 8 : 16) * g);
     const uint32_t v_at1 = ring + kTile * D + swizzled(tau<D>(2 * c + 1) * (D == 64 ? 64 : 128) + (D == 64 ? 8 : 16) * g);

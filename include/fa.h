@@ -29,6 +29,10 @@
  * Mask: causal masks key j for query i when j > i + N_k - N (j > i when
  * N_k = N).  A row with no allowed key gets O = 0, lse = -inf.
  *
+ * Further down: rotary positions (fa_rotary_init, fa_rope) and a paged key/value
+ * cache in 8 bits (fa_cache_append, fa_cache_attn, fa_cache_gather), whose
+ * layouts are given there.
+ *
  * Ownership: the caller owns every buffer.  The library allocates, frees and
  * synchronises nothing (except fa_read_device_status and fa_fwd_host, which
  * say so), holds no state beyond a per-device cache of properties (and the two
@@ -498,14 +502,16 @@ FA_EXPORT size_t fa_cache_attn_workspace_bytes(const fa_cache_attn_params *p);
 
 /*
  * fa_cache_attn -- attention of a few query tokens for each sequence over the
- * cache, O and lse as in fa_fwd.  Made for decoding: the keys are split
- * evenly over the whole GPU whatever the sequences' lengths, each key and
- * value is read once for all the query heads that share it, and the parts are
- * merged by a second launch.  For the many tokens of a prompt, fa_fwd_ex on
- * the contiguous keys (fa_cache_gather) is the faster call.  Sums, softmax
- * statistics and products accumulate in fp32; the weights are rounded to
- * fp16 before the product with the values.  A row with no allowed key gets
- * O = 0, lse = -inf.  The keys of a page outside [0, n_pages) are left out
+ * cache, O and lse as in fa_fwd.  Made for decoding: each key and value is read
+ * once for the query heads that share it (for up to 16 rows of heads and
+ * tokens; once more for each further 16, 8 for d = 256).  The keys are split evenly
+ * over the whole GPU whatever the sequences' lengths, and the parts are merged by a
+ * second launch; few sequences that can hold few tokens (by max_pages) are
+ * taken whole by clusters, in one launch.  For the many tokens of a prompt,
+ * fa_fwd_ex on the contiguous keys (fa_cache_gather) is the faster call.  Sums,
+ * softmax statistics and products accumulate in fp32; the weights are rounded to fp16
+ * (by at most 2^-11 of a weight) before the product with the values.  A row with
+ * no allowed key gets O = 0, lse = -inf.  The keys of a page outside [0, n_pages) are left out
  * and FA_ERR_BAD_PAGE is stored.  Results do not depend on timing.
  */
 FA_EXPORT fa_status fa_cache_attn(const fa_cache_attn_params *p, void *stream);
