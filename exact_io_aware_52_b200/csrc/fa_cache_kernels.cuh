@@ -46,15 +46,11 @@ struct AppendParams {
 
 constexpr int kMinScaleExp = -100;
 
-// 2^e with the least e >= kMinScaleExp such that amax <= 448 * 2^e, for a finite
-// amax >= 0: with amax = m * 2^E, 1 <= m < 2, and 448 = 1.75 * 2^8, e is E - 8
-// where m <= 1.75 and E - 7 else.  E comes from the exponent field (a
-// subnormal amax gives E = -127, under the limit either way).
-__device__ __forceinline__ float page_scale(float amax) {
-    const uint32_t u = __float_as_uint(amax);
-    int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u);
-    e = max(e, kMinScaleExp);
-    return __uint_as_float((uint32_t)(e + 127) << 23);
+// The exponent field of the scale for values of magnitude amax (a float's bits): 2^e with the least
+// e >= kMinScaleExp such that amax <= 448 * 2^e.  With amax = m * 2^E, 1 <= m < 2, and 448 = 1.75 * 2^8, e is
+// E - 8 where m <= 1.75 and E - 7 else: adding what a mantissa just above 1.75 needs to carry gives that.
+__device__ __forceinline__ uint32_t scale_field(uint32_t amax) {
+    return (uint32_t)max((int)((amax + 0x1fffffu) >> 23) - 8, 127 + kMinScaleExp);
 }
 
 // Four values times inv as E4M3 codes.  NaN gives the code NaN; SPECIAL: infinities
@@ -110,12 +106,17 @@ struct ScaleUpdate {
     bool grows;  // the page's earlier codes have to follow
 };
 __device__ __forceinline__ ScaleUpdate update_scale(bool held, float before, uint32_t amax) {
-    const float mine = page_scale(__uint_as_float(amax));
+    const uint32_t field = scale_field(amax);
     ScaleUpdate r;
-    r.now = held ? fmaxf(before, mine) : mine;
-    r.grows = held && r.now != before;
-    // a power of two from 2^-100 on, whose inverse is exact; the caller's own scale may be anything
-    r.inv = r.now == mine ? __uint_as_float(0x7f000000u - __float_as_uint(mine)) : 1.f / r.now;
+    r.now = __uint_as_float(field << 23);
+    r.inv = __uint_as_float((254u - field) << 23);
+    r.grows = false;
+    if (held) {  // the caller's own scale may be anything
+        const float mine = r.now;
+        r.now = fmaxf(before, mine);
+        r.grows = r.now != before;
+        if (r.now != mine) r.inv = 1.f / r.now;
+    }
     return r;
 }
 
@@ -179,13 +180,14 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 __device__ __forceinline__ uint32_t key_amax(const float (&v)[16]) {
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(v[j]));
+    for (int j = 0; j < 16; j += 2) asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[j]), "f"(v[j + 1]));
     return __float_as_uint(m);
 }
 __device__ __forceinline__ uint32_t value_amax(const Raw16 &x) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(x.w[j] & 0x7fff7fffu));
+    for (int j = 0; j < 8; ++j) asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x.w[j]));
+    m &= 0x7fff7fffu;  // (the signs are those of the products)
     return max(m << 16, m & 0xffff0000u);
 }
 // Of the finite ones.
@@ -242,7 +244,7 @@ __device__ __forceinline__ void rescale_run(uint8_t *run, float ratio) {
 template <bool VEC, bool TWO>
 __global__ void __launch_bounds__(1024, 1) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
     extern __shared__ float4 s_cs[];  // [token][pair of entries][slot]: (cos, sin) of two of a slot's 8 entries
-    __shared__ uint2 s_max[2][32];
+    __shared__ uint32_t s_max[3][2];  // of K and V, of three heads in turn
     constexpr bool AHEAD = VEC && !TWO;
     constexpr int CHUNKS = TWO ? 2 : 1;
     const CacheView &c = p.c;
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(1024, 1) fa_cache_append_kernel(const __grid_c
     const int pt = u % p.pages, b = u / p.pages;
     Touched pg;
     if (!touched_page(p, b, pt, threadIdx.x == 0, pg)) return;
+    if (threadIdx.x < 6) s_max[threadIdx.x >> 1][threadIdx.x & 1] = 0;
     const int dim = VEC ? p.dim : 0;
     const int per_row = c.d >> 4, row_log2 = 31 - __clz(per_row);
     const int turned = dim >> 4;  // slots of a token that are turned
@@ -291,9 +294,9 @@ __global__ void __launch_bounds__(1024, 1) fa_cache_append_kernel(const __grid_c
                 rotary_cs(step[rotary_pair(e, j + 1, dim, p.interleaved)], pos, p.amplitude, 1.f, x.z, x.w);
                 s_cs[q * turned + e] = x;
             }
-            __syncthreads();
         }
     }
+    __syncthreads();
     const float4 *my_cs = s_cs + i * 4 * turned + slot;
     // The key of this thread's slot, turned.
     auto key = [&](int chunk, float (&k)[16]) {
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(1024, 1) fa_cache_append_kernel(const __grid_c
                 k[j] = key_component(p, xk + chunk * dt * p.xs[0][2], 16 * slot + j, (int)(pg.lo + pg.s0 + i + chunk * dt));
         }
     };
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int turn = 0;
 
     for (int h = h0; h < h1; ++h) {
         float k[16];
@@ -334,15 +337,21 @@ __global__ void __launch_bounds__(1024, 1) fa_cache_append_kernel(const __grid_c
             xv += p.xs[1][1];
             if (h + 1 < h1) load(0);
         }
-        uint2 *sm = s_max[h & 1];  // the other one may still be read for the head before
+        // the maximum of the block.  Its place was last read a barrier ago when it is cleared, and is
+        // next used after the following barrier.
         auto block_max = [&]() {
             mk = __reduce_max_sync(0xffffffffu, mk);
             mv = __reduce_max_sync(0xffffffffu, mv);
-            if ((threadIdx.x & 31) == 0) sm[warp] = make_uint2(mk, mv);
+            if ((threadIdx.x & 31) == 0) {
+                atomicMax(&s_max[turn][0], mk);
+                atomicMax(&s_max[turn][1], mv);
+            }
             __syncthreads();
-            const uint2 x = sm[threadIdx.x & (warps - 1)];
-            mk = __reduce_max_sync(0xffffffffu, x.x);
-            mv = __reduce_max_sync(0xffffffffu, x.y);
+            mk = s_max[turn][0];
+            mv = s_max[turn][1];
+            const int before = turn == 0 ? 2 : turn - 1;
+            if (threadIdx.x == 0) s_max[before][0] = s_max[before][1] = 0;
+            turn = turn == 2 ? 0 : turn + 1;
         };
         // read by all before thread 0 writes them
         const float before_k = pg.s0 > 0 ? c.k_scale[unit] : 0.f, before_v = pg.s0 > 0 ? c.v_scale[unit] : 0.f;
@@ -363,7 +372,6 @@ __global__ void __launch_bounds__(1024, 1) fa_cache_append_kernel(const __grid_c
                 mk = max(mk, amax_finite(k));
                 mv = max(mv, amax_finite(y));
             }
-            __syncthreads();
             block_max();
         }
         const ScaleUpdate uk = update_scale(pg.s0 > 0, before_k, mk), uv = update_scale(pg.s0 > 0, before_v, mv);
