@@ -158,17 +158,20 @@ def rope(rotary, q, k=None, *, pos=None, pos0=0, inverse=False, out_dtype=None, 
     dev = q.get_device()
     if not isinstance(rotary, Rotary):
         _refuse("rotary must be a Rotary")
-    sq = _heads(q, "q", dev)
-    B, H, N, d = q.shape
-    x_type = _DTYPES.get(q.dtype)
+    B, H, N, d = q.shape  # (ValueError for other numbers of dimensions)
+    sq = q.stride()
+    if dev < 0 or (sq[3] != 1 and d > 1):
+        _refuse("q must be a CUDA tensor whose heads have contiguous components")
+    x_dtype = q.dtype
+    x_type = _DTYPES.get(x_dtype)
     if k is not None:
-        sk = _heads(k, "k", dev)
         Bk, Hk, Nk, dk = k.shape
-        if Bk != B or Nk != N or dk != d or k.dtype is not q.dtype:
-            _refuse("k must be [B, H_kv, N, d] of q's dtype")
+        sk = k.stride()
+        if Bk != B or Nk != N or dk != d or k.dtype is not x_dtype or k.get_device() != dev or (sk[3] != 1 and d > 1):
+            _refuse("k must be [B, H_kv, N, d] of q's dtype, on its device, with contiguous components")
     if out is None:
         yq = yk = None
-        y_dtype = q.dtype if out_dtype is None else out_dtype
+        y_dtype = x_dtype if out_dtype is None else out_dtype
     else:
         yq, yk = (out, None) if k is None else out
         y_dtype = yq.dtype
@@ -201,15 +204,15 @@ def rope(rotary, q, k=None, *, pos=None, pos0=0, inverse=False, out_dtype=None, 
     syq = yq.stride()
     if k is None:
         p = _pack(_ROPE, q.data_ptr(), yq.data_ptr(), H, sq[0], sq[1], sq[2], syq[0], syq[1], syq[2],
-                       0, 0, 0, 0, 0, 0, 0, 0, 0,
-                       B, N, d, x_type, y_type, pos_at, pos_stride, pos0, 1 if inverse else 0, rotary._address)
+                  0, 0, 0, 0, 0, 0, 0, 0, 0,
+                  B, N, d, x_type, y_type, pos_at, pos_stride, pos0, 1 if inverse else 0, rotary._address)
     else:
         if yk is None:
             yk = _empty(B, Hk, N, d, y_dtype)
         syk = yk.stride()
         p = _pack(_ROPE, q.data_ptr(), yq.data_ptr(), H, sq[0], sq[1], sq[2], syq[0], syq[1], syq[2],
-                       k.data_ptr(), yk.data_ptr(), Hk, sk[0], sk[1], sk[2], syk[0], syk[1], syk[2],
-                       B, N, d, x_type, y_type, pos_at, pos_stride, pos0, 1 if inverse else 0, rotary._address)
+                  k.data_ptr(), yk.data_ptr(), Hk, sk[0], sk[1], sk[2], syk[0], syk[1], syk[2],
+                  B, N, d, x_type, y_type, pos_at, pos_stride, pos0, 1 if inverse else 0, rotary._address)
     st = _call("fa_rope")(p, _raw_stream(dev))
     if st:
         raise fb.FaError(st, "fa_rope")

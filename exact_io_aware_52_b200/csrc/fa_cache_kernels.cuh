@@ -232,6 +232,11 @@ __device__ __forceinline__ void rescale_run(uint8_t *run, float ratio) {
     *reinterpret_cast<uint4 *>(run) = w;
 }
 
+// `runs` runs of 16 codes of a page that grows, by the whole block.  Rare, and kept out of the kernel's registers.
+__device__ __noinline__ void rescale_codes(uint8_t *codes, int runs, float ratio) {
+    for (int r = threadIdx.x; r < runs; r += blockDim.x) rescale_run(codes + 16 * r, ratio);
+}
+
 // One block per (sequence, touched page, group of heads): it owns the page's codes and scales of
 // its heads, so that nothing needs atomics and no order of blocks changes the result.
 // The sines and cosines, several times the work of the rest, are computed once for a group
@@ -389,14 +394,8 @@ __global__ void __launch_bounds__(1024, 1) fa_cache_append_kernel(const __grid_c
             store_slot(c.v + off + chunk * dt * c.d, plain_slot(slot), y, uv.inv, special_v);
         }
         // the tokens from before, by exact ratios for powers of two
-        if (uk.grows) {
-            uint8_t *page = c.k + (long long)unit * c.page * c.d;
-            for (int r = threadIdx.x; r < pg.s0 * per_row; r += blockDim.x) rescale_run(page + 16 * r, before_k * uk.inv);
-        }
-        if (uv.grows) {
-            uint8_t *page = c.v + (long long)unit * c.page * c.d;
-            for (int r = threadIdx.x; r < pg.s0 * per_row; r += blockDim.x) rescale_run(page + 16 * r, before_v * uv.inv);
-        }
+        if (uk.grows) rescale_codes(c.k + (long long)unit * c.page * c.d, pg.s0 * per_row, before_k * uk.inv);
+        if (uv.grows) rescale_codes(c.v + (long long)unit * c.page * c.d, pg.s0 * per_row, before_v * uv.inv);
         if (threadIdx.x == 0) {
             if (pg.s0 == 0 || uk.grows) c.k_scale[unit] = uk.now;
             if (pg.s0 == 0 || uv.grows) c.v_scale[unit] = uv.now;
