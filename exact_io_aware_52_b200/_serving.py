@@ -106,6 +106,8 @@ def _elsewhere(dev, stream):
         return torch.cuda.device(dev)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    if stream.device_index != dev:
+        _refuse("stream belongs to another device than the tensors")
     return torch.cuda.stream(stream)
 
 

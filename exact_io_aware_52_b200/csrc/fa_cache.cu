@@ -181,7 +181,7 @@ fa_status set_attn_smem(int dev) {
     static std::atomic<bool> ready[kMaxDevices];
     if (ready[dev].load(std::memory_order_acquire)) return FA_OK;
     if (cudaFuncSetAttribute(fa::cattn::fa_cache_attn_kernel<D, NT, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             fa::cattn::kSmemBytes<D, WARPS>) != cudaSuccess)
+                             fa::cattn::kSmemBytes<D, NT, WARPS>) != cudaSuccess)
         return FA_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
     return FA_OK;
@@ -197,7 +197,7 @@ fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(kp.c.B * kp.c.H_kv * kp.chunks * n));
         cfg.blockDim = dim3(32 * W);
-        cfg.dynamicSmemBytes = ca::kSmemBytes<D, W>;
+        cfg.dynamicSmemBytes = ca::kSmemBytes<D, NT, W>;
         cfg.stream = s;
         cudaLaunchAttribute at;
         at.id = cudaLaunchAttributeClusterDimension;
@@ -213,7 +213,7 @@ fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_
     const int warps = kp.chunks * kp.workers, ctas = ca::kResident<D, NT> * sms;
     const int full = (warps + ca::kWarps - 1) / ca::kWarps;
     ca::fa_cache_attn_kernel<D, NT, ca::kWarps>
-        <<<full > ctas ? full : (warps < ctas ? warps : ctas), 32 * ca::kWarps, ca::kSmemBytes<D, ca::kWarps>, s>>>(kp);
+        <<<full > ctas ? full : (warps < ctas ? warps : ctas), 32 * ca::kWarps, ca::kSmemBytes<D, NT, ca::kWarps>, s>>>(kp);
     if (cudaPeekAtLastError() != cudaSuccess) return FA_ERR_CUDA;
 
     // The merge is launched while the first kernel runs and waits in it for its results.  A pair

@@ -57,10 +57,14 @@ template <int D> constexpr int kStep = D == 64 ? 2 : 1;
 template <int D> constexpr int kStages = D == 64 ? 4 : 3;
 // CTAs for each SM.  More tiles in flight are not better: d = 128 with one CTA more or a tile
 // more in the ring took 5 to 15 % longer.
-template <int D, int NT> constexpr int kResident = D == 64 ? (NT == 2 ? 3 : 4) : (D == 128 && NT < 2 ? 3 : 2);
+template <int D, int NT> constexpr int kResident = D == 64 ? (NT == 2 ? 3 : 4) : (D == 128 ? 3 : 2);
 template <int D> constexpr int kStageBytes = 2 * kTile * D;  // codes of K and V
 template <int D> constexpr int kRingBytes = kStages<D> * kStageBytes<D>;
-template <int D, int WARPS> constexpr int kSmemBytes = WARPS * kRingBytes<D> + 1024;  // the rings begin on a swizzle atom
+// 16 rows of d = 128 leave too few registers for the queries: they are read from shared memory for each tile.
+template <int D, int NT> constexpr int kQueryBytes = D == 128 && NT == 2 ? NT * (D / 16) * 256 : 0;
+template <int D, int NT> constexpr int kWarpBytes = kRingBytes<D> + kQueryBytes<D, NT>;
+template <int D, int NT, int WARPS>
+constexpr int kSmemBytes = WARPS * kWarpBytes<D, NT> + 1024;  // the rings begin on a swizzle atom
 // tau(r) in four bits for each of 8 rows r: found by trying the orders for one in which neither the
 // lanes' reads of K (16 bytes) nor those of V (16, or 8 for d = 64) meet in a bank.  d = 64 has two
 // tokens in a 128-byte line, d = 256 half a token.
@@ -258,7 +262,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     // NT = 0: at most 4 rows, in the products' even columns: one for each lane of a group of 4, so that the
     // softmax has no idle half.  Else 8 NT rows, two for each lane of a group and product.
     constexpr int CH = T == 1 ? 2 : 1;       // sums that a tile's scores are split into
-    constexpr bool PACK = NT == 0;
+    constexpr bool PACK = NT == 0, QS = kQueryBytes<D, NT> > 0;
     constexpr int G = PACK ? 1 : NT, RL = PACK ? 1 : 2, R = rows_of(NT);
     static_assert(S % T == 0 && 32 % T == 0, "steps do not straddle the ring's end or a window's");
 
@@ -285,7 +289,8 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         locate(p, plan, at, b, first);
     }
 
-    const uint32_t ring = ((smem_u32(smem_raw) + 1023) & ~1023u) + warp * kRingBytes<D>;
+    const uint32_t ring = ((smem_u32(smem_raw) + 1023) & ~1023u) + warp * kWarpBytes<D, NT>;
+    const uint32_t q_at = ring + kRingBytes<D> + 8 * lane;  // QS: [row block][step][lane] operands
     uint64_t *bar = s_bar[warp];
     if (lane == 0) {
         for (int i = 0; i < S; ++i) mbar_init(&bar[i], 1);
@@ -398,7 +403,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     while (more) {
         // ---- queries: fp16 of each row times a power of two that brings its largest magnitude
         // to [2^14, 2^15); bf16's 8 bits stay exact but for components 2^-28 below the row's largest
-        uint32_t qf[G][D / 16][2];
+        uint32_t qf[QS ? 1 : G][QS ? 1 : D / 16][2];
         float rs[G][RL];   // of this lane's rows: scale * log2(e) / that power
         int lim[G][RL];    // and their number of keys
 #pragma unroll
@@ -433,11 +438,19 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
             for (int j = 0; j < KJ; ++j)
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t z = raw[j][2 * w + i];
-                        qf[t][4 * j + w][i] = pack_half2(bf16x2_lo(z) * up, bf16x2_hi(z) * up);
+                {
+                    const uint32_t z0 = raw[j][2 * w], z1 = raw[j][2 * w + 1];
+                    const uint32_t a = pack_half2(bf16x2_lo(z0) * up, bf16x2_hi(z0) * up);
+                    const uint32_t b2 = pack_half2(bf16x2_lo(z1) * up, bf16x2_hi(z1) * up);
+                    if constexpr (QS) {  // read by this lane alone
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_at + (t * (D / 16) + 4 * j + w) * 256),
+                                     "r"(a), "r"(b2)
+                                     : "memory");
+                    } else {
+                        qf[t][4 * j + w][0] = a;
+                        qf[t][4 * j + w][1] = b2;
                     }
+                }
             const float f = __uint_as_float((uint32_t)(127 - e) << 23) * p.scale_log2;
 #pragma unroll
             for (int i = 0; i < RL; ++i) {
@@ -526,8 +539,14 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                         half4(aw[w], a0, a2);
                         half4(bw[w], a1, a3);
 #pragma unroll
-                        for (int t = 0; t < G; ++t)
-                            mma16816(s[u][t][w % CH], a0, a1, a2, a3, qf[t][4 * j + w][0], qf[t][4 * j + w][1]);
+                        for (int t = 0; t < G; ++t) {
+                            uint2 q;
+                            if constexpr (QS)
+                                q = lds8(q_at + (t * (D / 16) + 4 * j + w) * 256);
+                            else
+                                q = make_uint2(qf[t][4 * j + w][0], qf[t][4 * j + w][1]);
+                            mma16816(s[u][t][w % CH], a0, a1, a2, a3, q.x, q.y);
+                        }
                     }
             }
             // ---- scores in units of log2 of this lane's rows: [i] of token tau(g), [RL + i] of tau(g) + 8
@@ -694,11 +713,11 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         if constexpr (DIRECT) {
             // ---- the warps' parts, normalised, in their rings, and their merge
             constexpr int RS = D + 4;
-            static_assert(R * RS * 4 <= kRingBytes<D>, "the rows lie in the warp's ring");
+            static_assert(R * RS * 4 <= kWarpBytes<D, NT>, "the rows lie in the warp's shared memory");
             __shared__ float2 s_ml[WARPS][R], s_row[R];
             __shared__ __align__(16) float s_o[R][D];
             uint8_t *const base = smem_raw + (((smem_u32(smem_raw) + 1023) & ~1023u) - smem_u32(smem_raw));
-            float *rows = reinterpret_cast<float *>(base + warp * kRingBytes<D>);
+            float *rows = reinterpret_cast<float *>(base + warp * kWarpBytes<D, NT>);
             __syncwarp();  // every lane has read its last tile
 #pragma unroll
             for (int t = 0; t < G; ++t)
@@ -733,7 +752,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) {
                     const float a = ex2_approx(s_ml[w][r].x - ref) * s_ml[w][r].y;
-                    const float4 y = *reinterpret_cast<const float4 *>(base + w * kRingBytes<D> + 4 * (r * RS + d0));
+                    const float4 y = *reinterpret_cast<const float4 *>(base + w * kWarpBytes<D, NT> + 4 * (r * RS + d0));
                     sum += a;
                     o.x += a * y.x, o.y += a * y.y, o.z += a * y.z, o.w += a * y.w;
                 }
