@@ -156,7 +156,6 @@ struct Plan {
     int total, per;
     int own, sum;  // scan_costs of the first 32 sequences
 };
-template <int D>
 __device__ __forceinline__ Plan make_plan(const Params &p) {
     Plan r;
     scan_costs(p, 0, r.own, r.sum);
@@ -173,6 +172,7 @@ __device__ __forceinline__ Plan make_plan(const Params &p) {
 // The sequence that holds place x < total of the line, and where it begins.
 __device__ __forceinline__ void locate(const Params &p, const Plan &plan, int x, int &b, int &first) {
     int before = 0, own = plan.own, sum = plan.sum;
+    first = 0;
     for (b = 0;; b += 32) {
         const unsigned hit = __ballot_sync(0xffffffffu, before + sum > x);
         if (hit) {
@@ -285,7 +285,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     const int row0 = chunk * R;
     int per = 0, at = 0, end = 0, b = 0, first = 0;
     if constexpr (!DIRECT) {
-        const Plan plan = make_plan<D>(p);
+        const Plan plan = make_plan(p);
         per = plan.per;
         if ((long long)worker * per >= plan.total) return;
         at = worker * per;
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps<WPR>) fa_cache_merge_kernel(c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * (WARPS / WPR) + warp / WPR;
     const int sub = warp % WPR;
-    const Plan plan = make_plan<D>(p);
+    const Plan plan = make_plan(p);
     const int unit = (int)(row / p.rows), r = (int)(row - (long long)unit * p.rows);
     const int b = unit / p.c.H_kv, h = unit - b * p.c.H_kv;
     const bool inside = b < p.c.B;

@@ -288,6 +288,24 @@ def test_append_infinities_nan_zeros_and_extremes():
         assert torch.isnan(got).sum() == 3 and ws.min() == 2.0 ** -100
 
 
+@pytest.mark.parametrize("shape", [(1, 200, 1, 256, 128, [5], None), (2, 1, 2, 128, 64, [3, 64], None), (1, 70, 2, 128, 64, [0], None)])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_append_infinities_in_every_kernel(shape, offset):
+    """Pages read twice, few tokens, and heads without infinities next to heads with them."""
+    def special(x):
+        x[0, 0, 0, 0, 7] = math.inf
+        x[0, -1, 1, -1, 9] = -math.inf
+        x[0, -1, 0, 0, 11] = math.nan
+    B, N, H_kv, d, page, start, n_new = shape
+    pool, dpool, k, v, n = run_append(47, *shape, x_of=special, offset=offset)
+    for codes, scales, x, gc, gs in ((pool[0], pool[2], k, dpool[0], dpool[2]), (pool[1], pool[3], v, dpool[1], dpool[3])):
+        wc, ws = as64(codes), scales.to(F64).clone()
+        ref.append(wc, ws, pool[4], x.to(F64), start, n, page)
+        assert torch.equal(gs.cpu().to(F64), ws)
+        got = as64(gc)
+        assert torch.equal(torch.isnan(got), torch.isnan(wc)) and torch.equal(got.nan_to_num(), wc.nan_to_num())
+
+
 def test_append_behind_a_scale_of_zero():
     """A page whose scale is 0 holds zeros whatever its codes are, also when it gets a scale."""
     H_kv, d, page = 1, 64, 16
