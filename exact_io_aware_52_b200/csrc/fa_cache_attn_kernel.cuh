@@ -124,6 +124,14 @@ __device__ __forceinline__ float2 peer_float2(uint32_t addr, int rank) {
     return r;
 }
 
+// What turns acc into O, 2^(n - m - 7) / sum, as two factors, each near its square root: for value scales far
+// below 1 the whole is below the normal fp32 values, which ex2.approx.ftz makes 0, although O is not.
+__device__ __forceinline__ float2 out_factor(float m, float n, float sum) {
+    if (sum == 0.f) return make_float2(0.f, 0.f);
+    const float half = ex2_approx(0.5f * (n - m - 7.f));
+    return make_float2(half / sum, half);
+}
+
 __device__ __forceinline__ float row_lse(float m, float l) {
     return l == 0.f ? neg_inf() : ((m == neg_inf() ? 0.f : m) + log2f(l)) * 0.693147180559945f;
 }
@@ -732,15 +740,15 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                     sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                     if (failed) sum = __int_as_float(0x7fffffff);
-                    const float f = sum == 0.f ? 0.f : ex2_approx(n[t][k] - m[t][k] - 7.f) / sum;
+                    const float2 f = out_factor(m[t][k], n[t][k], sum);
                     const int r = PACK ? c : 8 * t + 2 * c + k;
                     if (g == 0) s_ml[warp][r] = make_float2(m[t][k], sum);
 #pragma unroll
                     for (int w = 0; w < D / 32; ++w) {
                         const int d0 = D == 64 ? 8 * g + 4 * w : 128 * (w >> 2) + 16 * g + 4 * (w & 3);
                         *reinterpret_cast<float4 *>(rows + r * RS + d0) =
-                            make_float4(acc[t][2 * w][k] * f, acc[t][2 * w][k + 2] * f, acc[t][2 * w + 1][k] * f,
-                                        acc[t][2 * w + 1][k + 2] * f);
+                            make_float4(acc[t][2 * w][k] * f.x * f.y, acc[t][2 * w][k + 2] * f.x * f.y,
+                                        acc[t][2 * w + 1][k] * f.x * f.y, acc[t][2 * w + 1][k + 2] * f.x * f.y);
                     }
                 }
             __syncthreads();
@@ -813,7 +821,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 if (failed) sum = __int_as_float(0x7fffffff);
-                const float f = sum == 0.f ? 0.f : ex2_approx(n[t][k] - m[t][k] - 7.f) / sum;
+                const float2 f = out_factor(m[t][k], n[t][k], sum);
                 const int r = PACK ? c : 8 * t + 2 * c + k;
                 if (row0 + r >= p.rows) continue;
                 if (g == 0) {
@@ -826,8 +834,8 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w) {
                     const int d0 = D == 64 ? 8 * g + 4 * w : 128 * (w >> 2) + 16 * g + 4 * (w & 3);
-                    const float4 o = make_float4(acc[t][2 * w][k] * f, acc[t][2 * w][k + 2] * f,
-                                                 acc[t][2 * w + 1][k] * f, acc[t][2 * w + 1][k + 2] * f);
+                    const float4 o = make_float4(acc[t][2 * w][k] * f.x * f.y, acc[t][2 * w][k + 2] * f.x * f.y,
+                                                 acc[t][2 * w + 1][k] * f.x * f.y, acc[t][2 * w + 1][k + 2] * f.x * f.y);
                     if (whole)
                         store_out(p, (row + r) * D + d0, o);
                     else

@@ -471,7 +471,9 @@ typedef struct {
 FA_EXPORT fa_status fa_cache_gather(const fa_cache_gather_params *p, void *stream);
 
 typedef struct {
-    fa_cache cache;            /* scales: finite, >= 0                                   */
+    fa_cache cache;            /* scales: finite, >= 0, subnormal ones included.  The sums
+                                  over the keys are fp32: values (code * scale) of more
+                                  than 2^88 in magnitude may overflow them               */
     const void *q;             /* device bf16 [B, H, N, d], contiguous, 16-byte aligned  */
     void *o;                   /* device [B, H, N, d], fp32 or bf16 per o_dtype          */
     float *lse;                /* device fp32 [B, H, N]                                  */
