@@ -211,7 +211,9 @@ fa_status fa_rotary_init(fa_rotary *r, const fa_rotary_spec *sp) {
     if (!r || !sp) return FA_ERR_INVALID_ARGUMENT;
     if (sp->dim < 2 || sp->dim > FA_ROTARY_MAX_DIM || (sp->dim & 1)) return FA_ERR_INVALID_ARGUMENT;
     if (sp->layout != FA_ROTARY_HALF && sp->layout != FA_ROTARY_INTERLEAVED) return FA_ERR_INVALID_ARGUMENT;
-    if (!std::isfinite(sp->amplitude) || sp->amplitude < 0.0) return FA_ERR_INVALID_ARGUMENT;
+    // as the kernels hold it: what fp32 makes an infinity, or 0 of something else, is refused too
+    const float amplitude = sp->amplitude == 0.0 ? 1.f : (float)sp->amplitude;
+    if (!std::isfinite(amplitude) || amplitude <= 0.f) return FA_ERR_INVALID_ARGUMENT;
     const long double two_pi = 6.283185307179586476925286766559L;
     long double w[FA_ROTARY_MAX_DIM / 2];
     if (sp->angles) {
@@ -248,7 +250,7 @@ fa_status fa_rotary_init(fa_rotary *r, const fa_rotary_spec *sp) {
     std::memset(r, 0, sizeof *r);
     r->dim = sp->dim;
     r->layout = sp->layout;
-    r->amplitude = sp->amplitude == 0.0 ? 1.f : (float)sp->amplitude;
+    r->amplitude = amplitude;
     for (int i = 0; i < sp->dim / 2; ++i) {
         long double t = w[i] / two_pi;
         t -= std::floor(t);

@@ -343,7 +343,7 @@ typedef struct {
     double factor;           /* > 0, finite; unused by FA_ROTARY_NONE                   */
     double original_length;  /* FA_ROTARY_PARTS: > 0                                    */
     double low_turns, high_turns; /* FA_ROTARY_PARTS: 0 <= low < high                   */
-    double amplitude;        /* m above; 0 means 1; finite, >= 0                        */
+    double amplitude;        /* m above; 0 means 1; else > 0 and finite as fp32          */
     const double *angles;    /* host, w_i in radians for each of the dim / 2 pairs, or
                                 NULL.  If given, base and scaling are not used; finite,
                                 |w_i| <= 2^20                                           */

@@ -1,0 +1,33 @@
+"""The rotation's handle and what a call refuses before anything is launched, without a GPU."""
+import ctypes
+import math
+
+import pytest
+
+import exact_io_aware_52_b200 as fa
+from exact_io_aware_52_b200 import _binding as fb
+from exact_io_aware_52_b200 import build as fbuild
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    fbuild.build()
+
+
+@pytest.mark.parametrize("amplitude", [1e39, 3.5e38, 1.7e308, 1e-50, 5e-324, 2.0 ** -151])
+def test_rotary_refuses_amplitudes_outside_fp32(amplitude):
+    """The kernels hold the amplitude in fp32: what becomes an infinity or zero there is refused."""
+    with pytest.raises(fb.FaError) as e:
+        fa.Rotary(64, amplitude=amplitude)
+    assert e.value.status == fb.FA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("amplitude", [1e38, 3.4028234e38, 2.0 ** -149, 0.7])
+def test_rotary_keeps_amplitudes_of_fp32(amplitude):
+    got = fa.Rotary(64, amplitude=amplitude).struct.amplitude
+    assert math.isfinite(got) and abs(got - amplitude) <= 2.0 ** -24 * amplitude
+
+
+def test_rotary_amplitude_zero_means_one():
+    r, spec = fb.FaRotary(), fb.FaRotarySpec(dim=64, base=10000.0, amplitude=0.0)
+    assert fb.load().fa_rotary_init(ctypes.byref(r), ctypes.byref(spec)) == fb.FA_OK and r.amplitude == 1.0
