@@ -146,6 +146,13 @@ class Rotary:
         self.layout = layout
         self._address = ctypes.addressof(self.struct)
 
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_address"}
+
+    def __setstate__(self, state):  # of a copy, which has a table of its own
+        self.__dict__.update(state)
+        self._address = ctypes.addressof(self.struct)
+
 
 def rope(rotary, q, k=None, *, pos=None, pos0=0, inverse=False, out_dtype=None, out=None, stream=None):
     """fa_rope: the heads of q (and k, in the same launch) turned by their positions.
@@ -228,7 +235,8 @@ class PagedCache:
     64 or 128, d 64, 128 or 256.  k_scale, v_scale: fp32 [n_pages, H_kv].
     table: int32 [B, max_pages]: token t of sequence b lies in slot t % page
     of page table[b, t // page]; entries past a sequence's end are not read.  What the
-    tensors hold may change between calls; their places may not.
+    tensors hold may change between calls; their places may not: for other tensors make
+    another PagedCache (assigning to this one's is refused).  A deep copy has copies of the tensors.
     """
 
     def __init__(self, k, v, k_scale, v_scale, table):
@@ -245,6 +253,7 @@ class PagedCache:
                 (table.shape[1] > 1 and table.stride(1) != 1)):
             _refuse("table must be int32 [B, max_pages] on the same device, contiguous along the pages")
         self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
+        self._workspace = {}  # (H, N) -> bytes
         self.device_index = dev
         self.n_pages, self.H_kv, self.page, self.d = k.shape
         self.B, self.max_pages = table.shape
@@ -253,7 +262,17 @@ class PagedCache:
         self._packed = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                    table.data_ptr(), table.stride(0), self.n_pages, self.max_pages, self.B, self.H_kv,
                                    self.page, self.d)
-        self._workspace = {}  # (H, N) -> bytes
+
+    def __setattr__(self, name, value):
+        if "_packed" in self.__dict__:
+            raise AttributeError("a PagedCache is for the tensors that it was made of: make another one for others")
+        super().__setattr__(name, value)
+
+    def __getstate__(self):
+        return self.k, self.v, self.k_scale, self.v_scale, self.table
+
+    def __setstate__(self, tensors):  # of a copy: its addresses are its own tensors'
+        self.__init__(*tensors)
 
 
 def cache_append(cache, k, v, start, *, n_new=None, rotary=None, dev_status=None, stream=None):

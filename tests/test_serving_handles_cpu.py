@@ -1,6 +1,9 @@
 """The rotation's handle and what a call refuses before anything is launched, without a GPU."""
+import copy
 import ctypes
+import gc
 import math
+import pickle
 
 import pytest
 
@@ -31,3 +34,19 @@ def test_rotary_keeps_amplitudes_of_fp32(amplitude):
 def test_rotary_amplitude_zero_means_one():
     r, spec = fb.FaRotary(), fb.FaRotarySpec(dim=64, base=10000.0, amplitude=0.0)
     assert fb.load().fa_rotary_init(ctypes.byref(r), ctypes.byref(spec)) == fb.FA_OK and r.amplitude == 1.0
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+def test_copies_of_a_rotation_have_their_own_table(how):
+    """A call passes the address of the table: a copy that outlives the rotation it was made from has to pass
+    that of a table that lives as long as itself."""
+    r = fa.Rotary(64, layout="interleaved", amplitude=1.5, base=500.0)
+    want = bytes(r.struct)
+    c = {"copy": copy.copy, "deepcopy": copy.deepcopy, "pickle": lambda x: pickle.loads(pickle.dumps(x))}[how](r)
+    assert c._address == ctypes.addressof(c.struct) and bytes(c.struct) == want
+    assert (c.dim, c.layout) == (64, "interleaved")
+    del r
+    gc.collect()
+    again = [fa.Rotary(64, base=7.0) for _ in range(64)]  # takes the freed table's place, if there is one
+    assert ctypes.string_at(c._address, len(want)) == want
+    del again
