@@ -290,6 +290,7 @@ fa_status fa_rope(const fa_rope_params *p, void *stream) {
             ++in_place;
         }
     }
+    if (!p->pos && (long long)p->pos0 + p->N - 1 > 0x7fffffffLL) return FA_ERR_INVALID_ARGUMENT;
     if (!fa_detail::aligned(p->pos, 4)) return FA_ERR_MISALIGNED;
     int dev = 0, num_sms = 0;
     if ((st = fa_detail::current_device(&dev, &num_sms)) != FA_OK) return st;

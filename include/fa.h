@@ -382,7 +382,7 @@ typedef struct {
     int B, N, d;             /* d: rotary dim .. FA_ROPE_MAX_D                          */
     int x_dtype, y_dtype;    /* fa_dtype                                                */
     const int32_t *pos;      /* device int32 positions, pos[b * pos_stride + n], or NULL:
-                                the position of token n is pos0 + n                     */
+                                the position of token n is pos0 + n (below 2^31)        */
     int64_t pos_stride;      /* 0: one row of positions for the whole batch             */
     int32_t pos0;
     int inverse;             /* 1: turn by the negative angles (with the amplitude, the

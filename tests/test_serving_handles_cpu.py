@@ -50,3 +50,26 @@ def test_copies_of_a_rotation_have_their_own_table(how):
     again = [fa.Rotary(64, base=7.0) for _ in range(64)]  # takes the freed table's place, if there is one
     assert ctypes.string_at(c._address, len(want)) == want
     del again
+
+
+# ---------------------------------------------------------------- refusals of fa_rope
+def _rope_status(t0=None, **kw):
+    p = fb.FaRopeParams(B=2, N=8, d=64, x_dtype=0, y_dtype=0, rotary=ctypes.pointer(fa.Rotary(64).struct))
+    p.t[0] = fb.FaRopeTensor(x=0x10000, y=0x20000, heads=4)
+    p.t[0].x_stride[:] = p.t[0].y_stride[:] = (2048, 512, 64)
+    for k, v in (t0 or {}).items():
+        if k.endswith("stride"):
+            getattr(p.t[0], k)[:] = v
+        else:
+            setattr(p.t[0], k, v)
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return fb.load().fa_rope(ctypes.byref(p), None)
+
+
+def test_rope_refuses_positions_past_int32():
+    """Token n is at pos0 + n, which must not wrap around."""
+    last = 2 ** 31 - 1
+    assert _rope_status(pos0=last - 6) == fb.FA_ERR_INVALID_ARGUMENT
+    assert _rope_status(pos0=last) == fb.FA_ERR_INVALID_ARGUMENT
+    assert _rope_status(pos0=last, N=0) == fb.FA_OK  # no token (nothing is launched)
