@@ -282,9 +282,11 @@ fa_status fa_rope(const fa_rope_params *p, void *stream) {
         vec = vec && vectors(t.x, t.x_stride, p->B, t.heads, p->N, xb) &&
               vectors(t.y, t.y_stride, p->B, t.heads, p->N, yb);
         ++present;
+        const int n[3] = {p->B, t.heads, p->N};
+        for (int i = 0; i < 3; ++i)
+            if (n[i] > 1 && t.y_stride[i] == 0) return FA_ERR_INVALID_ARGUMENT;  // several results for one place
         if (t.x == t.y) {
             if (p->x_dtype != p->y_dtype) return FA_ERR_INVALID_ARGUMENT;
-            const int n[3] = {p->B, t.heads, p->N};
             for (int i = 0; i < 3; ++i)
                 if (n[i] > 1 && t.x_stride[i] != t.y_stride[i]) return FA_ERR_INVALID_ARGUMENT;
             ++in_place;

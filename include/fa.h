@@ -374,7 +374,7 @@ typedef struct {
     int heads;               /* >= 0; 0: the tensor is absent                           */
     int64_t x_stride[3];     /* elements from one batch element, head, token to the next
                                 (components are contiguous); any order of dimensions    */
-    int64_t y_stride[3];
+    int64_t y_stride[3];     /* not 0 in a dimension of several entries                 */
 } fa_rope_tensor;
 
 typedef struct {

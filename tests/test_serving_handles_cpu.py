@@ -73,3 +73,11 @@ def test_rope_refuses_positions_past_int32():
     assert _rope_status(pos0=last - 6) == fb.FA_ERR_INVALID_ARGUMENT
     assert _rope_status(pos0=last) == fb.FA_ERR_INVALID_ARGUMENT
     assert _rope_status(pos0=last, N=0) == fb.FA_OK  # no token (nothing is launched)
+
+
+@pytest.mark.parametrize("t0", [
+    dict(y_stride=(0, 512, 64)), dict(y_stride=(2048, 0, 64)), dict(y_stride=(2048, 512, 0)),
+    dict(y=0x10000, x_stride=(0, 512, 64), y_stride=(0, 512, 64)),  # in place: turned once for each batch element
+])
+def test_rope_refuses_outputs_whose_entries_share_a_place(t0):
+    assert _rope_status(t0) == fb.FA_ERR_INVALID_ARGUMENT
