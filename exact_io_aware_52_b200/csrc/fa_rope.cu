@@ -271,7 +271,8 @@ fa_status fa_rope(const fa_rope_params *p, void *stream) {
     if (st != FA_OK) return st;
     const long long rows = (long long)p->B * p->N, heads = (long long)p->t[0].heads + p->t[1].heads;
     if (rows == 0 || heads == 0) return FA_OK;
-    if (rows > 0x7fffffffLL || heads > 65535) return FA_ERR_INVALID_ARGUMENT;
+    // rows are counted in 32 bits, with those that a last block has no work for
+    if (rows > 0x7fffffffLL - (fa::kRopeThreads - 1) || heads > 65535) return FA_ERR_INVALID_ARGUMENT;
     const int xb = elem_bytes(p->x_dtype), yb = elem_bytes(p->y_dtype);
     bool vec = p->d % 16 == 0 && p->rotary->dim % 16 == 0;
     int in_place = 0, present = 0;

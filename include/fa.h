@@ -378,8 +378,9 @@ typedef struct {
 } fa_rope_tensor;
 
 typedef struct {
-    fa_rope_tensor t[2];     /* queries and keys, say; one launch turns both            */
-    int B, N, d;             /* d: rotary dim .. FA_ROPE_MAX_D                          */
+    fa_rope_tensor t[2];     /* queries and keys, say; one launch turns both; 65535
+                                heads at most together                                  */
+    int B, N, d;             /* d: rotary dim .. FA_ROPE_MAX_D; B * N <= 2^31 - 256     */
     int x_dtype, y_dtype;    /* fa_dtype                                                */
     const int32_t *pos;      /* device int32 positions, pos[b * pos_stride + n], or NULL:
                                 the position of token n is pos0 + n (below 2^31)        */

@@ -81,3 +81,9 @@ def test_rope_refuses_positions_past_int32():
 ])
 def test_rope_refuses_outputs_whose_entries_share_a_place(t0):
     assert _rope_status(t0) == fb.FA_ERR_INVALID_ARGUMENT
+
+
+def test_rope_refuses_more_rows_than_its_grid_counts():
+    """The grid is counted in 32 bits, with up to 255 rows of a block behind the last one."""
+    for B, N in ((1, 2 ** 31 - 1), (1, 2 ** 31 - 255), (2 ** 31 - 255, 1), (2 ** 16, 2 ** 15)):
+        assert _rope_status(B=B, N=N) == fb.FA_ERR_INVALID_ARGUMENT
