@@ -17,8 +17,10 @@ namespace fa {
 
 // cos and sin of position * step, times the amplitude.  The angle's nearest quarter
 // turn leaves at most an eighth of a turn x, where sin x = x + x^3 S(x^2) and
-// cos x = 1 - x^2 / 2 + x^4 C(x^2) with S and C of degree 2, fitted for this file to the least
-// maximum error on [0, pi / 4] (2^-28 and 2^-33); evaluated in fp32 both err by at most 2^-23.8.
+// cos x = 1 - x^2 / 2 + x^4 C(x^2) with S and C of degree 2, fitted for this file on [0, pi / 4] by Lawson's
+// iteration (weighted least squares towards the least maximum error), S for the error relative to the sine, C for
+// the absolute one of the cosine.  Rounded to fp32 the coefficients leave 2^-26.8 of the sine (2^-27.3 of 1) and 2^-30.9;
+// with every step in fp32, from the 32-bit angle on, both err by at most 2^-23.2 of 1.
 // About 30 instructions for both, two thirds of what sincospif takes.
 __device__ __forceinline__ void rotary_cs(uint64_t step, int pos, float amplitude, float sign, float &c, float &s) {
     const uint32_t angle = (uint32_t)((step * (uint64_t)(int64_t)pos) >> 32);  // in 2^-32 turns
