@@ -176,23 +176,23 @@ fa_status launch_merge(const fa::cattn::Params &kp, int rows_per, cudaStream_t s
                                                                                                        : FA_ERR_CUDA;
 }
 
-template <int D, int NT, int WARPS>
+template <int D, int NT, int WARPS, bool FINE>
 fa_status set_attn_smem(int dev) {
     static std::atomic<bool> ready[kMaxDevices];
     if (ready[dev].load(std::memory_order_acquire)) return FA_OK;
-    if (cudaFuncSetAttribute(fa::cattn::fa_cache_attn_kernel<D, NT, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             fa::cattn::kSmemBytes<D, NT, WARPS>) != cudaSuccess)
+    if (cudaFuncSetAttribute(fa::cattn::fa_cache_attn_kernel<D, NT, WARPS, FINE>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, fa::cattn::kSmemBytes<D, NT, WARPS>) != cudaSuccess)
         return FA_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
     return FA_OK;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool FINE>
 fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_t s) {
     namespace ca = fa::cattn;
     constexpr int W = ca::kDirectWarps<D, NT>;
     if (const int n = kp.cluster) {
-        const fa_status st = set_attn_smem<D, NT, W>(dev);
+        const fa_status st = set_attn_smem<D, NT, W, FINE>(dev);
         if (st != FA_OK) return st;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(kp.c.B * kp.c.H_kv * kp.chunks * n));
@@ -205,14 +205,14 @@ fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_
         at.val.clusterDim.y = at.val.clusterDim.z = 1;
         cfg.attrs = &at;
         cfg.numAttrs = n > 1 ? 1 : 0;
-        return cudaLaunchKernelEx(&cfg, ca::fa_cache_attn_kernel<D, NT, W>, kp) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+        return cudaLaunchKernelEx(&cfg, ca::fa_cache_attn_kernel<D, NT, W, FINE>, kp) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     }
-    const fa_status st = set_attn_smem<D, NT, ca::kWarps>(dev);
+    const fa_status st = set_attn_smem<D, NT, ca::kWarps, FINE>(dev);
     if (st != FA_OK) return st;
     // few workers are spread over the SMs, one warp in a CTA at work
     const int warps = kp.chunks * kp.workers, ctas = ca::kResident<D, NT> * sms;
     const int full = (warps + ca::kWarps - 1) / ca::kWarps;
-    ca::fa_cache_attn_kernel<D, NT, ca::kWarps>
+    ca::fa_cache_attn_kernel<D, NT, ca::kWarps, FINE>
         <<<full > ctas ? full : (warps < ctas ? warps : ctas), 32 * ca::kWarps, ca::kSmemBytes<D, NT, ca::kWarps>, s>>>(kp);
     if (cudaPeekAtLastError() != cudaSuccess) return FA_ERR_CUDA;
 
@@ -224,13 +224,18 @@ fa_status launch_attn(const fa::cattn::Params &kp, int dev, int sms, cudaStream_
     return launch_merge<D, 32>(kp, ca::rows_of(NT), s);
 }
 
+template <int D, bool FINE>
+fa_status launch_attn_rows(const fa::cattn::Params &kp, int nt, int dev, int sms, cudaStream_t s) {
+    if constexpr (D < 256) {
+        if (nt == 2) return launch_attn<D, 2, FINE>(kp, dev, sms, s);
+    }
+    return launch_attn<D, 1, FINE>(kp, dev, sms, s);
+}
+
 template <int D>
 fa_status launch_attn_d(const fa::cattn::Params &kp, int nt, int dev, int sms, cudaStream_t s) {
-    if (nt == 0) return launch_attn<D, 0>(kp, dev, sms, s);
-    if constexpr (D < 256) {
-        if (nt == 2) return launch_attn<D, 2>(kp, dev, sms, s);
-    }
-    return launch_attn<D, 1>(kp, dev, sms, s);
+    if (nt == 0) return launch_attn<D, 0, true>(kp, dev, sms, s);
+    return kp.o_bf16 ? launch_attn_rows<D, false>(kp, nt, dev, sms, s) : launch_attn_rows<D, true>(kp, nt, dev, sms, s);
 }
 
 }  // namespace

@@ -9,7 +9,8 @@
 // value lies more than 2^8 above them: m for l = sum_j 2^(x_j - m), and n for
 // acc = sum_j 2^(x_j + log2(vs_j) - n + 7) v'_j.  The second keeps the weights of
 // the product with the codes inside fp16 whatever the pages' scales are (largest
-// 2^15, and 2^-24 the step of the smallest); O = acc * 2^(n - m - 7) / l.
+// 2^15, and 2^-24 the step of the smallest: a weight errs by 2^-25 too, where the largest is
+// 2^7 or more, that is by 2^-32 of it); O = acc * 2^(n - m - 7) / l.
 //
 // Tiles.  A warp takes 16 tokens of one key/value head at a time.  S^T = K Q^T and
 // O^T = V^T P^T are computed transposed (tokens or components
@@ -243,6 +244,16 @@ __device__ __forceinline__ uint32_t transposed8x8(uint32_t a) {
     return r;
 }
 
+// A value's first 11 bits, which fp16 holds (from 2^-14 on).
+__device__ __forceinline__ float upper11(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+
+// The sums of the weights' two parts, of the even and the odd columns.
+template <int D>
+__device__ __forceinline__ void join_halves(float (&acc)[D / 16][4]) {
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) acc[d][0] += acc[d][1], acc[d][2] += acc[d][3];
+}
+
 // Words of V codes of one lane: [token][word], tokens tau(2c), tau(2c + 1) of the tile and those 8 further on.
 template <int D> using VWords = uint32_t[4][D / 32];
 
@@ -262,7 +273,14 @@ __device__ __forceinline__ bool has_nan_code(uint32_t w) { return ((w & 0x7f7f7f
 // Direct (kDirectWarps): a cluster of CTAs takes one pair, its warps parts of the pair's
 // tiles, which are merged in shared memory, the CTA's first and then the cluster's: one launch and
 // no partial results in memory, for lengths at which that counts.
-template <int D, int NT, int WARPS>
+//
+// A weight is fp32 until its product with the codes, which takes fp16.  FINE: it goes there as the sum of two
+// fp16 numbers, its first 11 bits and the rest, so that O keeps fp32's precision (2^-20 of a weight instead of 2^-11).
+// Up to 4 rows that costs nothing (the rests are the columns that are empty otherwise) and is always so.  With more rows the
+// rests have products of their own, for fp32 outputs only: a bf16 output is itself off by 8 times 2^-11.
+// Measured, fp32 outputs with and without, us: 16 rows of d = 128 105 / 96 and of d = 64 76 / 70, 8 rows of d = 64 52 / 49,
+// of d = 128 78 / 80 and of d = 256 92 / 87, 56 rows of d = 128 326 / 286.
+template <int D, int NT, int WARPS, bool FINE>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == kWarps ? kResident<D, NT> : 1)
 fa_cache_attn_kernel(const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -274,7 +292,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
     // NT = 0: at most 4 rows, in the products' even columns: one for each lane of a group of 4, so that the
     // softmax has no idle half.  Else 8 NT rows, two for each lane of a group and product.
     constexpr int CH = T == 1 ? 2 : 1;       // sums that a tile's scores are split into
-    constexpr bool PACK = NT == 0, QS = kQueryBytes<D, NT> > 0;
+    constexpr bool PACK = NT == 0, TWICE = FINE && !PACK, QS = kQueryBytes<D, NT> > 0;
     constexpr int G = PACK ? 1 : NT, RL = PACK ? 1 : 2, R = rows_of(NT);
     static_assert(S % T == 0 && 32 % T == 0, "steps do not straddle the ring's end or a window's");
 
@@ -612,10 +630,11 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                         for (int d = 0; d < D / 16; ++d) {
                             acc[t][d][k] *= fa;
                             acc[t][d][k + 2] *= fa;
+                            if constexpr (PACK) acc[t][d][1] *= fa, acc[t][d][3] *= fa;
                         }
                     }
             }
-            uint32_t pb[T][G][2];
+            uint32_t pb[T][G][2], pl[TWICE ? T : 1][TWICE ? G : 1][2];
 #pragma unroll
             for (int u = 0; u < T; ++u)
 #pragma unroll
@@ -626,9 +645,19 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                         l[t][k % RL] += ex2_approx(x[u][t][k] + m0[t][k % RL]);
                         w[k] = ex2_approx(x[u][t][k] + (lv[u] + n0[t][k % RL]));
                     }
-                    // PACK: column 2 c has row c, column 2 c + 1 nothing
-                    pb[u][t][0] = transposed8x8(pack_half2(w[0], PACK ? 0.f : w[1]));
-                    pb[u][t][1] = transposed8x8(pack_half2(w[RL], PACK ? 0.f : w[2 * RL - 1]));
+                    if constexpr (PACK) {  // column 2 c has the first bits of row c, column 2 c + 1 the rest
+                        pb[u][t][0] = transposed8x8(pack_half2(upper11(w[0]), w[0] - upper11(w[0])));
+                        pb[u][t][1] = transposed8x8(pack_half2(upper11(w[1]), w[1] - upper11(w[1])));
+                    } else {
+                        if constexpr (TWICE) {
+                            pl[u][t][0] = transposed8x8(pack_half2(w[0] - upper11(w[0]), w[1] - upper11(w[1])));
+                            pl[u][t][1] = transposed8x8(pack_half2(w[2] - upper11(w[2]), w[3] - upper11(w[3])));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) w[k] = upper11(w[k]);
+                        }
+                        pb[u][t][0] = transposed8x8(pack_half2(w[0], w[1]));
+                        pb[u][t][1] = transposed8x8(pack_half2(w[2], w[3]));
+                    }
                 }
 
             // ---- O^T
@@ -694,6 +723,8 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
                                     for (int k = 0; k < 2; ++k) {
                                         float part[4] = {0.f, 0.f, 0.f, 0.f};
                                         mma16816(part, a[k][0], a[k][1], a[k][2], a[k][3], pb[u][t][0], pb[u][t][1]);
+                                        if constexpr (TWICE)
+                                            mma16816(part, a[k][0], a[k][1], a[k][2], a[k][3], pl[u][t][0], pl[u][t][1]);
 #pragma unroll
                                         for (int j = 0; j < 4; ++j)
                                             if ((row0 + (PACK ? c : 8 * t + 2 * c + (j & 1))) % p.N == tq) acc[t][2 * w + k][j] += part[j];
@@ -710,6 +741,13 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                                 for (int k = 0; k < 2; ++k)
                                     mma16816(acc[t][2 * w + k], a[k][0], a[k][1], a[k][2], a[k][3], pb[u][t][0], pb[u][t][1]);
+                            if constexpr (TWICE) {
+#pragma unroll
+                                for (int t = 0; t < G; ++t)
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k)
+                                        mma16816(acc[t][2 * w + k], a[k][0], a[k][1], a[k][2], a[k][3], pl[u][t][0], pl[u][t][1]);
+                            }
                         }
                     }
                 }
@@ -730,6 +768,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
             __shared__ __align__(16) float s_o[R][D];
             uint8_t *const base = smem_raw + (((smem_u32(smem_raw) + 1023) & ~1023u) - smem_u32(smem_raw));
             float *rows = reinterpret_cast<float *>(base + warp * kWarpBytes<D, NT>);
+            if constexpr (PACK) join_halves<D>(acc[0]);
             __syncwarp();  // every lane has read its last tile
 #pragma unroll
             for (int t = 0; t < G; ++t)
@@ -811,6 +850,7 @@ fa_cache_attn_kernel(const __grid_constant__ Params p) {
         const bool whole = t0 == 0 && n_own == nb;
         const long long part = ((((long long)chunk * p.workers + worker) * 2) + (t0 == 0 ? 1 : 0)) * R;
         n_own = 0;
+        if constexpr (PACK) join_halves<D>(acc[0]);
         more = !failed && next_pair();
 #pragma unroll
         for (int t = 0; t < G; ++t)

@@ -512,8 +512,9 @@ FA_EXPORT size_t fa_cache_attn_workspace_bytes(const fa_cache_attn_params *p);
  * second launch; few sequences that can hold few tokens (by max_pages) are
  * taken whole by clusters, in one launch.  For the many tokens of a prompt,
  * fa_fwd_ex on the contiguous keys (fa_cache_gather) is the faster call.  Sums,
- * softmax statistics and products accumulate in fp32; the weights are rounded to fp16
- * (by at most 2^-11 of a weight) before the product with the values.  A row with
+ * softmax statistics and products accumulate in fp32.  For the product with the codes a weight
+ * (times its page's value scale) is rounded by at most 2^-20 of itself, for FA_O_BF16 and more than 4
+ * rows of heads and tokens by at most 2^-11; besides that by at most 2^-32 of the row's largest.  A row with
  * no allowed key gets O = 0, lse = -inf.  The keys of a page outside [0, n_pages) are left out
  * and FA_ERR_BAD_PAGE is stored.  Results do not depend on timing.
  */

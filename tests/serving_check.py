@@ -6,9 +6,12 @@ Bounds, for a row with scores x_j, weights p_j (their sum 1), page scales ks, vs
 * score: q in fp16 is exact for these inputs, k' is exact, the products are exact in the
   tensor core, and each of the up to 16 + 3 sums of a chain is off by at most 2^-23 of the sum of the magnitudes; four
   factors by 2^-24: e_x = 2^-18 sum_i |q_i k_i| scale;
-* weight: 2 e_x (numerator and sum), its rounding to fp16, 2^-11, and (|x| + |log2 vs| + 32) 2^-22 for
-  the exponential, the logarithm of the scale and the references, which are numbers of that size in fp32;
-* fp32 sums over at most 512 tiles of a warp, 2^-14, and over the lanes, the merge and its factors, 2^-14;
+* weight: 2 e_x (numerator and sum), its rounding, and (|x| + |log2 vs| + 32) 2^-22 for
+  the exponential, the logarithm of the scale and the references, which are numbers of that size in fp32.  The rounding is
+  to two fp16 numbers (11 bits cut off, the rest below 2^-10 rounded by 2^-11 of itself: 2^-20 is above that), and to one, 2^-11,
+  for bf16 outputs of more than 4 rows for each key;
+* fp32 sums over the tiles of a warp, 16 tokens each and at most 512 of them, each off by 2^-23 (so is the sum of the
+  weights), and over the lanes, the merge and its factors, less than 2^6 of them: 2^-17;
 * a weight that is subnormal in fp16 errs by half of its step, 2^-25, where the row's largest p_j vs_j is at
   least 2^7: 2^-32 max_j (p_j vs_j) for each code;
 * half a step of the output type, which below its smallest normal number 2^-126 is 2^-150 for fp32 (23 bits below
@@ -61,13 +64,15 @@ def attend_terms(q, pool, lens, causal, scale, page):
             mag[b, :, i] = (torch.einsum("hd,hnd->hn", qi.abs(), k[:, :m].abs()) * scale).amax(-1)
             top[b, :, i] = ps.amax(-1)
             log_vs[b, :, i] = s[:, :m].clamp(min=2.0 ** -149).log2().abs().amax(-1)
-    return dict(o=o, lse=lse, oabs=oabs, codes=codes, mag=mag, top=top, log_vs=log_vs)
+    steps = torch.tensor([min(-(-n // 16), 512) for n in lens], dtype=F64)[:, None, None]
+    return dict(o=o, lse=lse, oabs=oabs, codes=codes, mag=mag, top=top, log_vs=log_vs, steps=steps, rows=H // H_kv * N)
 
 
 def bounds(t, dtype):
     """The bounds above for O (of that type) and lse."""
     e_x = t["mag"] * 2.0 ** -18
-    rel = 2 * e_x + 2.0 ** -11 + (1.5 * t["mag"] + t["log_vs"] + 32) * 2.0 ** -22 + 2.0 ** -13
+    weight = 2.0 ** -11 if dtype is BF16 and t["rows"] > 4 else 2.0 ** -20
+    rel = 2 * e_x + weight + (1.5 * t["mag"] + t["log_vs"] + 32) * 2.0 ** -22 + 2 * t["steps"] * 2.0 ** -23 + 2.0 ** -17
     o = rel[..., None] * (t["oabs"] + t["o"].abs()) + t["codes"] * (2.0 ** -32 * t["top"])[..., None]
     o = o + (o + t["o"].abs()) * (2.0 ** -8 if dtype is BF16 else 2.0 ** -24) + 2.0 ** -145 + (2.0 ** -134 if dtype is BF16 else 0.0)
     return o, e_x + 2.0 ** -14 + 2.0 ** -22 * t["lse"].abs()
