@@ -16,7 +16,9 @@
 // O^T = V^T P^T are computed transposed (tokens or components
 // on the 16 side, query rows on the 8 side), so that the 4 to 8 query rows
 // that share a key fill the tensor core's narrow side and the codes are the
-// A operand.  tcgen05 would want 128 rows: at 8 rows 15/16 of it would be idle.
+// A operand.  (tcgen05 could have 128 tokens or components on its large side in the same way, with the query rows as
+// its narrow one.  It takes its operands from shared or tensor memory, so that the codes of 128 tokens, 8 boxes of 16, would
+// have to be written there as fp16 first.  Up to 8 rows the reads bound the kernel as it is; for more the form is untried.)
 // Both run on fp16 (mma m16n8k16), to which the codes convert exactly.  (The E4M3 form of
 // mma, with the queries in two parts, took more instructions: 408 for each tile of d = 128 against 334.)
 // Every warp works by itself: it has a ring of tiles that TMA fills (one lane issues),
@@ -29,10 +31,11 @@
 // query rows that share it.  The same tiles fetched by 16-byte cp.async (64 bytes
 // of a key for each group of 4 lanes) stopped at 4.8 TB/s whatever was done with
 // them; TMA's requests reach the copy rate.  Measured, 32 query heads on 8 of d = 128, one token each: 64 ragged
-// sequences of up to 8192 tokens (547 MB) 95 us, 8 of 16384 to 131072 (1451 MB) 230 us or 6.3 TB/s, one of
+// sequences of up to 8192 tokens (547 MB) 96 us, 8 of 16384 to 131072 (1451 MB) 235 us or 6.2 TB/s, one of
 // 500 tokens 6.7 us.  About 8 us of the split form are its start (lengths, plan, page table, first tiles) and
-// the merge.  With 16 rows for each key (96 us for 394 MB) and at d = 64 (49 us for 198 MB, 8 rows) the
-// instructions for each tile bound it: conversions, scores and weights, 235 at d = 64.
+// the merge.  With 16 rows for each key (96 us for 394 MB) and at d = 64 (49 us for 198 MB, 8 rows) neither memory nor a
+// pipe is full: the instructions of a tile (conversions, scores and weights, 235 at d = 64) wait for one
+// another, and 12 to 16 warps an SM fill 38 to 47 % of the issue slots.
 #pragma once
 
 #include <cuda.h>

@@ -81,9 +81,9 @@ template <> struct RawSlot<float> {
 // all of them (they cost about as much as turning 4 heads); it has UN heads'
 // loads in flight.  The lanes of a warp lie along the components and then
 // along the tokens: whole 128-byte lines whichever way the strides run.
-// Measured: bf16 32 + 8 heads of 2 x 8192 tokens, d = 128, 58.5 us or 5.7 TB/s (64 registers;
-// 4 heads in flight with 80: 64 us; 16 or 20 heads a thread: 60); fp32 to bf16, 16 + 16 heads of 2 x 4097
-// tokens, half of d turned, 35.7 us or 5.6 TB/s (2 heads in flight: 38).
+// Measured: bf16 32 + 8 heads of 2 x 8192 tokens, d = 128, 58 us or 5.8 TB/s (64 registers, of which the compiler
+// spills 64 bytes; 4 heads in flight with 80: 64 us; 16 or 20 heads a thread: 60); fp32 to bf16, 16 + 16 heads of 2 x 4097
+// tokens, half of d turned, 34 us or 6.0 TB/s (2 heads in flight: 38).
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 2 ? 4 : 2)
 fa_rope_kernel(const __grid_constant__ RopeParams p) {
@@ -134,7 +134,9 @@ fa_rope_kernel(const __grid_constant__ RopeParams p) {
 }
 
 // Any dim, alignment and strides: one thread has one pair (or one component
-// past dim) of one token and head, element by element.
+// past dim) of one token and head, element by element.  Not made for speed: a sine and cosine for every
+// head and 2-byte accesses.  Measured: 16 + 16 heads of 2 x 4096 tokens in bf16, 20 of 80 components turned, 134 us (84 MB, 13 us at
+// the copy rate), 24 of 96 156 us; 32 of 128, which the kernel above takes, 26 us.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_any_kernel(const __grid_constant__ RopeParams p) {
     const int items = (p.dim >> 1) + (p.copy_tail ? p.d - p.dim : 0);

@@ -444,7 +444,8 @@ typedef struct {
  * tokens (slots below the first new one) are rescaled, which for
  * power-of-two scales is exact but for codes that become subnormal.  A page
  * whose slot 0 is written has no scale from before.  Infinities and NaN
- * become the code NaN.  Slots behind the last new token are left as they are.
+ * become the code NaN.  (Finite magnitudes from 1.9375 * 2^127 on are nearest to a code that stands for
+ * 2^128, which fp32 and bf16 read as infinity.)  Slots behind the last new token are left as they are.
  *
  * A token whose position is negative or past the table, or whose page is
  * outside [0, n_pages), is not written and FA_ERR_BAD_PAGE is stored in
