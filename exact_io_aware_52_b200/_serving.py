@@ -263,16 +263,23 @@ class PagedCache:
                                    table.data_ptr(), table.stride(0), self.n_pages, self.max_pages, self.B, self.H_kv,
                                    self.page, self.d)
 
+    # What a call takes from the tensors it was made of, or follows from them.
+    _FIXED = frozenset(("k", "v", "k_scale", "v_scale", "table", "device_index", "n_pages", "H_kv", "page", "d", "B",
+                        "max_pages", "_workspace", "_packed"))
+
     def __setattr__(self, name, value):
-        if "_packed" in self.__dict__:
+        if name in self._FIXED and "_packed" in self.__dict__:
             raise AttributeError("a PagedCache is for the tensors that it was made of: make another one for others")
         super().__setattr__(name, value)
 
     def __getstate__(self):
-        return self.k, self.v, self.k_scale, self.v_scale, self.table
+        more = {name: value for name, value in self.__dict__.items() if name not in self._FIXED}
+        return (self.k, self.v, self.k_scale, self.v_scale, self.table), more
 
-    def __setstate__(self, tensors):  # of a copy: its addresses are its own tensors'
-        self.__init__(*tensors)
+    def __setstate__(self, state):  # of a copy: its addresses are its own tensors'
+        tensors, more = state
+        PagedCache.__init__(self, *tensors)
+        self.__dict__.update(more)
 
 
 def cache_append(cache, k, v, start, *, n_new=None, rotary=None, dev_status=None, stream=None):

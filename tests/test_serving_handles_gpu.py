@@ -58,3 +58,21 @@ def test_a_cache_refuses_other_tensors(name):
     value = getattr(c, name)
     with pytest.raises(AttributeError):
         setattr(c, name, value.clone() if torch.is_tensor(value) else value)
+
+
+class Layer(fa.PagedCache):
+    """A program's own cache, with more than the package's."""
+
+    def __init__(self, index):
+        super().__init__(*(t.to(dev()) for t in ref.pool(62, [20], 1, 16, 64)))
+        self.index = index
+
+
+def test_a_cache_can_have_more():
+    c = Layer(7)
+    c.note = [1, 2]
+    for other in (copy.copy(c), copy.deepcopy(c)):
+        assert type(other) is Layer and other.index == 7 and other.note == [1, 2]
+        n = torch.tensor([20], dtype=torch.int32, device=dev())
+        assert all(torch.equal(a, b) for a, b in zip(fa.cache_gather(c, n, 20), fa.cache_gather(other, n, 20)))
+    c.index = 8
